@@ -22,7 +22,8 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "mi
 EXPORTS = ("gdn_version", "gdn_chunk_size", "gdn_fwd_workspace_size", "gdn_bwd_workspace_size",
            "gdn_fwd", "gdn_fwd_noalloc", "gdn_fwd_noalloc_status", "gdn_bwd", "gdn_decode",
            "gdn_device_status", "gdn_status_string", "gdn_trace_install", "gdn_kernel_name",
-           "gdn_set_wait_limit", "gdn_set_test_hook")
+           "gdn_set_wait_limit", "gdn_set_test_hook", "gdn_linrec_states_size", "gdn_linrec_fwd",
+           "gdn_linrec_bwd", "gdn_linrec_decode")
 GDN_TEST_STALL_COPY, GDN_TEST_FAIL_LAUNCH = 1, 2
 
 
@@ -41,6 +42,13 @@ class GdnDesc(ctypes.Structure):
 GDN_FLAG_PIECE_SCAN = 1
 GDN_FLAG_QK_L2NORM = 2
 GDN_FLAG_VALUE_SLICES = 4
+GDN_LINREC_COMPLEMENT = 1
+
+
+class GdnLinrecDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "D", "n_seqs", "x_stride", "g_stride",
+                                              "o_stride", "dx_stride", "dg_stride")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "g_dtype", "flags", "reserved")]
 
 
 _lock = threading.Lock()
@@ -77,6 +85,16 @@ def lib() -> ctypes.CDLL:
                                   fp, fp, vp, sz, vp]
             L.gdn_decode.restype = ctypes.c_int
             L.gdn_decode.argtypes = [dp, vp, vp, vp, fp, fp, fp, vp, vp]
+            lp = ctypes.POINTER(GdnLinrecDesc)
+            L.gdn_linrec_states_size.restype = sz
+            L.gdn_linrec_states_size.argtypes = [lp]
+            L.gdn_linrec_fwd.restype = ctypes.c_int
+            L.gdn_linrec_fwd.argtypes = [lp, vp, vp, i32p, i32p, fp, vp, fp, fp, vp]
+            L.gdn_linrec_bwd.restype = ctypes.c_int
+            L.gdn_linrec_bwd.argtypes = [lp, vp, vp, i32p, i32p, fp, vp, fp, vp, vp, fp, fp, vp,
+                                         sz, vp]
+            L.gdn_linrec_decode.restype = ctypes.c_int
+            L.gdn_linrec_decode.argtypes = [lp, vp, vp, fp, vp, vp]
             L.gdn_device_status.restype = ctypes.c_int
             L.gdn_device_status.argtypes = [vp, vp]
             L.gdn_status_string.restype = ctypes.c_char_p
@@ -239,6 +257,188 @@ def gdn_decode(q, k, v, g, beta, state, scale=1.0, o=None, stream=None, qk_l2nor
                       _ptr(state), _ptr(o), _stream(stream))
     if rc:
         raise GdnError(rc, "gdn_decode")
+    return o
+
+
+# ------------------------------------------------------- gated linear recurrence
+_DT = {torch.bfloat16: GDN_BF16, torch.float32: GDN_FP32}
+
+
+class _Here:
+    """The context of a call on the current device and stream: nothing to change."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def _scope(device, stream, used):
+    """(context, stream) of a call whose tensors live on ``device``: allocations and
+    launches go to ``stream`` (None: that device's current stream), whatever the current
+    device is; tensors used on another stream than the current one are recorded on it."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    cur = torch.cuda.current_stream(device)
+    if stream is None or stream == cur:
+        if torch.cuda.current_device() == device.index:
+            return _here, cur
+        return torch.cuda.stream(cur), cur
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    for t in used:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream), stream
+
+
+def _check_on(t, name, device, dtype=None, shape=None):
+    """_check, and that t lives on the call's device."""
+    _check(t, name, dtype, shape)
+    if t is not None and t.device != device:
+        raise ValueError("%s is on %s, the call's tensors on %s" % (name, t.device, device))
+
+
+def _row_stride(t, name, device, dtype, shape):
+    """Elements from one token to the next of a (B, T, ...) tensor whose values of one token
+    are adjacent and whose tokens are evenly spaced over all rows (a column slice of a wider
+    contiguous tensor is; a transposed or expanded one is not)."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, the call's tensors on %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.is_contiguous():
+        return 0
+    width = 1
+    for n, s in zip(reversed(shape[2:]), reversed(t.stride()[2:])):
+        if n > 1 and s != width:
+            raise ValueError("%s: the values of one token must be adjacent" % name)
+        width *= n
+    B, T = shape[:2]
+    s = t.stride(1) if T > 1 else t.stride(0) if B > 1 else width
+    if s < width or (B > 1 and T > 1 and t.stride(0) != T * s):
+        raise ValueError("%s: tokens must be evenly spaced over all rows, without overlap" % name)
+    return s
+
+
+def _linrec_desc(x, g, n_seqs, complement, do=None, o=None, dx=None, dg=None):
+    if x.dim() != 3:
+        raise ValueError("x must have shape (B, T, D), got %s" % (tuple(x.shape),))
+    if x.dtype not in _DT:
+        raise ValueError("x must be bf16 or fp32")
+    if g.dtype not in (x.dtype, torch.float32):
+        raise ValueError("g must be %s or torch.float32, got %s" % (x.dtype, g.dtype))
+    shape, dev = tuple(x.shape), x.device
+    row = lambda t, name, dt: 0 if t is None else _row_stride(t, name, dev, dt, shape)
+    return GdnLinrecDesc(*shape, n_seqs, row(x, "x", x.dtype), row(g, "g", g.dtype),
+                         row(do, "do", x.dtype) if do is not None else row(o, "o", x.dtype),
+                         row(dx, "dx", x.dtype), row(dg, "dg", g.dtype), _DT[x.dtype],
+                         _DT[g.dtype], GDN_LINREC_COMPLEMENT if complement else 0, 0)
+
+
+def gdn_linrec_fwd(x, g, cu_seqlens=None, h0=None, complement=False, output_final_state=True,
+                   save_states=False, o=None, hT=None, states=None, cu_seqlens_host=None,
+                   stream=None):
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + w_t x_t per channel, o = h (w = 1, or
+    1 - exp(g_t) with ``complement``), through the C ABI.  x, g: (B, T, D), which may be column
+    slices of a wider tensor; h0: (N, D) fp32.  Returns (o, hT), or (o, hT, states) with
+    ``save_states``: a buffer that spares gdn_linrec_bwd recomputing the states."""
+    L = lib()
+    dev = x.device
+    scope, stream = _scope(dev, stream, (x, g, h0, cu_seqlens, o, hT, states))
+    with scope:
+        cu_dev, cu_host = _seqlens(cu_seqlens, cu_seqlens_host, dev)
+        n_seqs = 0 if cu_host is None else cu_host.numel() - 1
+        desc = _linrec_desc(x, g, n_seqs, complement, o=o)
+        N = (n_seqs or x.shape[0], x.shape[2])
+        _check_on(h0, "h0", dev, torch.float32, N)
+        _check_on(hT, "hT", dev, torch.float32, N)
+        _check_on(cu_dev, "cu_seqlens", dev)
+        _check_on(states, "states", dev, torch.uint8)
+        if o is None:
+            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if hT is None and output_final_state:
+            hT = torch.empty(N, dtype=torch.float32, device=dev)
+        if save_states or states is not None:
+            need = L.gdn_linrec_states_size(ctypes.byref(desc))
+            if need == 0:
+                raise GdnError(1, "gdn_linrec_states_size")
+            if states is None:
+                states = torch.empty(need, dtype=torch.uint8, device=dev)
+            elif states.numel() < need:
+                raise GdnError(4, "gdn_linrec_fwd")
+        rc = L.gdn_linrec_fwd(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), _ptr(cu_dev),
+                              _ptr(cu_host), _ptr(h0), o.data_ptr(), _ptr(hT), _ptr(states),
+                              stream.cuda_stream)
+    if rc:
+        raise GdnError(rc, "gdn_linrec_fwd")
+    return (o, hT, states) if states is not None else (o, hT)
+
+
+def gdn_linrec_bwd(x, g, do, cu_seqlens=None, h0=None, dhT=None, complement=False, states=None,
+                   grads=None, workspace=None, cu_seqlens_host=None, stream=None, want_dh0=True):
+    """Gradients (dx, dg, dh0) of gdn_linrec_fwd for upstream ``do`` and ``dhT``, through the C
+    ABI.  ``states``: what gdn_linrec_fwd returned for the same x, g, cu_seqlens and h0; without
+    it the states are recomputed into the workspace."""
+    L = lib()
+    dev = x.device
+    dx, dg, dh0 = grads if grads is not None else (None, None, None)
+    scope, stream = _scope(dev, stream, (x, g, do, h0, dhT, cu_seqlens, dx, dg, dh0, states,
+                                         workspace))
+    with scope:
+        cu_dev, cu_host = _seqlens(cu_seqlens, cu_seqlens_host, dev)
+        n_seqs = 0 if cu_host is None else cu_host.numel() - 1
+        desc = _linrec_desc(x, g, n_seqs, complement, do=do, dx=dx, dg=dg)
+        N = (n_seqs or x.shape[0], x.shape[2])
+        for t, name in ((h0, "h0"), (dhT, "dhT"), (dh0, "dh0")):
+            _check_on(t, name, dev, torch.float32, N)
+        _check_on(cu_dev, "cu_seqlens", dev)
+        _check_on(states, "states", dev, torch.uint8)
+        _check_on(workspace, "workspace", dev, torch.uint8)
+        if grads is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
+            dh0 = torch.empty(N, dtype=torch.float32, device=dev) if want_dh0 else None
+        need = L.gdn_linrec_states_size(ctypes.byref(desc))
+        if need == 0:
+            raise GdnError(1, "gdn_linrec_states_size")
+        if states is not None:
+            if states.numel() < need:
+                raise GdnError(4, "gdn_linrec_bwd")
+        elif workspace is None:
+            workspace = alloc_workspace(need, dev)
+        rc = L.gdn_linrec_bwd(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), _ptr(cu_dev),
+                              _ptr(cu_host), _ptr(h0), do.data_ptr(), _ptr(dhT), _ptr(dx),
+                              _ptr(dg), _ptr(dh0), _ptr(states), _ptr(workspace),
+                              0 if workspace is None else workspace.numel(), stream.cuda_stream)
+    if rc:
+        raise GdnError(rc, "gdn_linrec_bwd")
+    return dx, dg, dh0
+
+
+def gdn_linrec_decode(x, g, state, complement=False, o=None, stream=None):
+    """One-token form through the C ABI: advances ``state`` ((B, D) fp32, in place) through the
+    T tokens of x and g ((B, T, D)) and returns o."""
+    L = lib()
+    dev = x.device
+    scope, stream = _scope(dev, stream, (x, g, state, o))
+    with scope:
+        desc = _linrec_desc(x, g, 0, complement, o=o)
+        _check_on(state, "state", dev, torch.float32, (x.shape[0], x.shape[2]))
+        if o is None:
+            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        rc = L.gdn_linrec_decode(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), state.data_ptr(),
+                                 o.data_ptr(), stream.cuda_stream)
+    if rc:
+        raise GdnError(rc, "gdn_linrec_decode")
     return o
 
 

@@ -182,6 +182,9 @@ enum KernelId : int32_t {
     kKTcPieceC,
     kKL2Norm,
     kKL2NormBack,
+    kKLinrecFwd,
+    kKLinrecBwd,
+    kKLinrecDecode,
     kKernelCount
 };
 

@@ -199,6 +199,82 @@ gdn_status gdn_bwd(const gdn_desc *desc, const void *q, const void *k, const voi
 gdn_status gdn_decode(const gdn_desc *desc, const void *q, const void *k, const void *v,
                       const float *g, const float *beta, float *state, void *o, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated linear recurrence: the per-channel (diagonal) sibling of the gated
+ * delta rule.  Per sequence and channel, with the state in fp32:
+ *
+ *     h_t = a_t h_{t-1} + w_t x_t,   a_t = exp(g_t),   o_t = h_t
+ *     w_t = 1, or 1 - a_t with GDN_LINREC_COMPLEMENT
+ *
+ * g is the log-decay, one value per token and channel (g <= 0 in use; -inf is
+ * a reset to w_t x_t; a positive g grows the state, and the products of the
+ * factors over up to 1024 tokens then have to stay below the fp32 maximum).
+ * A NaN or infinity stays in its channel and its sequence.
+ *
+ * Layouts: x, o, do_, dx [B][T][D] in dtype; g, dg [B][T][D] in g_dtype
+ * (GDN_FP32, or the same as dtype); h0, hT, dh0, dhT [N][D] fp32, contiguous.
+ * A token's D values are adjacent; the *_stride fields give the elements from
+ * one token to the next (row b, token t starts at (b * T + t) * stride), so
+ * that the inputs can be column slices of a wider projection; 0 means D.
+ * o_stride is that of o in the forward and of do_ in the backward.  Elements
+ * between D and the stride are neither read for their values nor written.
+ * All pointers are 16-byte aligned; D and the strides may be any size (multiples
+ * of 16 bytes are copied fastest).  Sequences are the B dense rows, or packed
+ * documents (cu_seqlens, cu_seqlens_host) with the rules of gdn_fwd; an empty
+ * document passes its state through (hT = h0, dh0 = dhT).  The device copy of
+ * cu_seqlens must hold the host mirror's values; no address outside the
+ * buffers is formed whatever it holds.  With T = 0 the states pass through.
+ * Outputs must not overlap inputs (hT == h0 and dh0 == dhT are refused).
+ *
+ * The functions use no workspace but the one named, need no initialisation,
+ * wait for nothing on the host when cu_seqlens_host is given, and can be
+ * captured into CUDA graphs; results do not change from run to run.  (Without
+ * the mirror cu_seqlens is copied to the host, which a capture refuses:
+ * GDN_ERR_INVALID_ARG.) */
+#define GDN_LINREC_COMPLEMENT 1
+
+typedef struct gdn_linrec_desc {
+    int64_t B;        /* rows (must be 1 when n_seqs > 0) */
+    int64_t T;        /* tokens per row; B * T < 2^31 */
+    int64_t D;        /* channels, 1 .. 2^20 */
+    int64_t n_seqs;   /* 0: B dense rows; > 0: packed documents given by cu_seqlens */
+    int64_t x_stride, g_stride, o_stride, dx_stride, dg_stride; /* 0 = D */
+    int32_t dtype;    /* gdn_dtype of x, o, do_, dx */
+    int32_t g_dtype;  /* gdn_dtype of g, dg: GDN_FP32 or dtype */
+    int32_t flags;    /* GDN_LINREC_COMPLEMENT or 0 */
+    int32_t reserved; /* must be 0 */
+} gdn_linrec_desc;
+
+/* Bytes of the `states` buffer that the forward can leave for the backward
+ * (the fp32 states entering every 128th token: 1/32 float per element), which
+ * is also the backward's workspace size (0 on a bad descriptor). */
+size_t gdn_linrec_states_size(const gdn_linrec_desc *desc);
+
+/* Forward: o, and hT and states where they are not NULL; h0 NULL means zero. */
+gdn_status gdn_linrec_fwd(const gdn_linrec_desc *desc, const void *x, const void *g,
+                          const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                          const float *h0, void *o, float *hT, float *states, void *stream);
+
+/* Backward of (o, hT) given do_ and dhT (NULL means zero):
+ *
+ *     e_t = do_t + a_{t+1} e_{t+1}  (+ dhT at the last token),   dx_t = w_t e_t
+ *     dg_t = a_t e_t h_{t-1}, or a_t e_t (h_{t-1} - x_t) with the complement
+ *     dh0 = a_1 e_1                                     (dh0 may be NULL)
+ *
+ * states is the buffer that gdn_linrec_fwd filled for the same descriptor, x,
+ * g, cu_seqlens and h0; with NULL the states are recomputed into the workspace
+ * (gdn_linrec_states_size bytes, 256-byte aligned; unused when states is given). */
+gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void *g,
+                          const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                          const float *h0, const void *do_, const float *dhT, void *dx, void *dg,
+                          float *dh0, const float *states, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* One-token form for inference: advances state [B][D] (fp32, in place) through
+ * the T tokens (usually 1) of each of the B rows; n_seqs must be 0, T >= 1. */
+gdn_status gdn_linrec_decode(const gdn_linrec_desc *desc, const void *x, const void *g,
+                             float *state, void *o, void *stream);
+
 /* Synchronises the stream, then returns and clears the device-side status
  * that the last gdn_fwd/gdn_bwd on this workspace recorded (GDN_OK,
  * GDN_ERR_TIMEOUT, or GDN_ERR_INVALID_ARG when the device copy of cu_seqlens

@@ -1,0 +1,327 @@
+"""Gated linear recurrence (gdn_linrec_fwd, gdn_linrec_bwd, gdn_linrec_decode) against the fp64
+token-by-token form of oracle/linrec.py, element by element.  Tolerances are the oracle's fp32 error
+bounds plus, for a bf16 result, half a step of its own rounding (2^-8 of the value)."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_99_b200 as gdn
+from oracle import linrec as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+TYPES = [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")]
+TINY = 2.0 ** -126  # results below the smallest normal fp32 may be flushed
+
+
+def draw(B, T, D, dtype="bf16", gate="bf16", N=None, seed=0, decay=0.1, state=True):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen)
+    N = B if N is None else N
+    x = r(B, T, D).to(DT[dtype])
+    g = (-torch.nn.functional.softplus(r(B, T, D)) * decay).to(DT[gate])
+    h0 = r(N, D) if state else None
+    return dict(x=x, g=g, h0=h0, do=r(B, T, D).to(DT[dtype]), dhT=r(N, D) if state else None)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, want, err, name):
+    half = torch.finfo(got.dtype).eps / 2 if got.dtype != torch.float32 else 2.0 ** -24
+    got = np64(got).reshape(want.shape)
+    tol = err + half * (np.abs(want) + err) + TINY
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), "%s: %d of %d off, first at %s: %r for %r +- %r" % (
+        name, bad.sum(), bad.size, tuple(np.argwhere(bad)[0]), got[bad][0], want[bad][0],
+        np.broadcast_to(tol, want.shape)[bad][0])
+
+
+def run_and_check(v, lengths=None, complement=False, bwd=True, on=lambda t: t.cuda(), **kw):
+    """fwd (with and without saved states), bwd (the same) and every output against the oracle."""
+    B, T, D = v["x"].shape
+    cu = None if lengths is None else np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    cu_t = None if cu is None else torch.tensor(cu, dtype=torch.int32)
+    N = B if cu is None else len(lengths)
+    segs = ref.segments(B, T, cu)
+    flat = lambda t: np64(t).reshape(B * T, D)
+    h0 = np.zeros((N, D)) if v["h0"] is None else np64(v["h0"])
+    dhT = np.zeros((N, D)) if v["dhT"] is None else np64(v["dhT"])
+    o, hT, _, eo, ehT, _ = ref.fwd(flat(v["x"]), flat(v["g"]), h0, segs, complement)
+    d = {k: None if t is None else (on(t) if k in ("x", "g", "do") else t.cuda()) for k, t in v.items()}
+    args = dict(cu_seqlens=None if cu is None else cu_t.cuda(), cu_seqlens_host=cu_t, h0=d["h0"],
+                complement=complement, **kw)
+    go, ghT = gdn.gdn_linrec_fwd(d["x"], d["g"], **args)
+    go2, ghT2, states = gdn.gdn_linrec_fwd(d["x"], d["g"], save_states=True, **args)
+    close(go, o, eo, "o")
+    close(ghT, hT, ehT, "hT")
+    assert torch.equal(go, go2) and torch.equal(ghT, ghT2)
+    if not bwd:
+        return go, ghT
+    want, err = ref.bwd(flat(v["x"]), flat(v["g"]), h0, flat(v["do"]), dhT, segs, complement)
+    one = gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], dhT=d["dhT"], states=states, **args)
+    two = gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], dhT=d["dhT"], **args)
+    for name, a, b, w, e in zip(("dx", "dg", "dh0"), one, two, want, err):
+        close(a, w, e, name)
+        assert torch.equal(a, b), name
+    return (go, ghT) + one
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 1), (2, 3, 5), (1, 15, 64), (1, 16, 66), (3, 17, 31),
+                                   (1, 127, 64), (2, 128, 72), (2, 129, 130), (1, 1030, 65),
+                                   (1, 2500, 128), (5, 40, 256), (70, 2, 33), (300, 1, 8)])
+def test_sizes(B, T, D, complement, types):
+    run_and_check(draw(B, T, D, *types, seed=B + T + D), complement=complement)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("lengths", [[1], [0, 5, 0, 0, 3, 0], [128, 128], [127, 1, 1, 127, 256, 0],
+                                     [1] * 200, [300, 1, 0, 700, 16, 15, 17], [0, 0, 2049]])
+def test_packed_documents(lengths, types):
+    v = draw(1, sum(lengths), 72, *types, N=len(lengths), seed=len(lengths))
+    run_and_check(v, lengths=lengths, complement=len(lengths) % 2 == 1)
+
+
+def test_many_documents_of_odd_lengths():
+    lengths = [int(n) for n in np.random.default_rng(3).integers(0, 60, size=150)]
+    run_and_check(draw(1, sum(lengths), 40, N=150, seed=3), lengths=lengths)
+
+
+def test_no_initial_and_final_states():
+    v = draw(2, 200, 48, state=False)
+    args = {k: t.cuda() for k, t in v.items() if t is not None}
+    o, hT = gdn.gdn_linrec_fwd(args["x"], args["g"], output_final_state=False)
+    assert hT is None
+    dx, dg, dh0 = gdn.gdn_linrec_bwd(args["x"], args["g"], args["do"], want_dh0=False)
+    assert dh0 is None
+    run_and_check(v)
+    for got, want in zip((o, dx, dg), run_and_check(v)[0:1] + run_and_check(v)[2:4]):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D,types", [(64, TYPES[0]), (65, TYPES[0]), (66, TYPES[1]), (65, TYPES[2])])
+def test_column_slices_of_a_wider_tensor(D, types):
+    """x, g and do inside rows of another width, with values beside them that must not be read, and
+    outputs into slices whose neighbours must not be written."""
+    def inside(t):
+        wide = torch.full(t.shape[:2] + (D + 24,), float("nan"), dtype=t.dtype, device="cuda")
+        wide[..., 8:8 + D] = t.cuda()
+        return wide[..., 8:8 + D]
+
+    v = draw(2, 150, D, *types, seed=D)
+    want = run_and_check(v)
+    got = run_and_check(v, on=inside)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    d = {k: t.cuda() for k, t in v.items()}
+    wide = [torch.full((2, 150, D + 24), 7.0, dtype=dt, device="cuda")
+            for dt in (d["x"].dtype, d["x"].dtype, d["g"].dtype)]
+    o, dx, dg = (w[..., 8:8 + D] for w in wide)
+    gdn.gdn_linrec_fwd(d["x"], d["g"], h0=d["h0"], o=o)
+    gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], h0=d["h0"], dhT=d["dhT"],
+                       grads=(dx, dg, torch.empty_like(d["h0"])))
+    for w, t in zip(wide, (want[0], want[2], want[3])):
+        assert torch.equal(w[..., 8:8 + D], t)
+        assert (w[..., :8] == 7).all() and (w[..., 8 + D:] == 7).all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_resets_strong_decays_and_growth(types):
+    """-inf gates (resets), gates far below the fp32 range of exp, and growing states."""
+    v = draw(1, 300, 40, *types, seed=9)
+    v["g"][0, 7::50] = -float("inf")
+    v["g"][0, 13::50] = -200.0
+    v["g"][0, 100:110] = 0.25
+    v["g"][0, 33] = 0.0
+    for complement in (False, True):
+        run_and_check(v, complement=complement)
+
+
+def test_non_finite_values_stay_in_their_channel_and_document():
+    lengths = [40, 100, 30]
+    v = draw(1, 170, 40, N=3, seed=5)
+    want = run_and_check(v, lengths=lengths)
+    v["x"][0, 60, 3] = float("nan")
+    v["x"][0, 20, 5] = float("inf")
+    v["do"][0, 90, 7] = float("nan")
+    d = {k: t.cuda() for k, t in v.items()}
+    cu = torch.tensor([0, 40, 140, 170], dtype=torch.int32)
+    kw = dict(cu_seqlens=cu.cuda(), cu_seqlens_host=cu, h0=d["h0"])
+    o, hT = gdn.gdn_linrec_fwd(d["x"], d["g"], **kw)
+    dx, dg, dh0 = gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], dhT=d["dhT"], **kw)
+    seq = torch.repeat_interleave(torch.arange(3), torch.tensor(lengths))
+    touched = {3: 1, 5: 0, 7: 1}
+    for got, ref_ in zip((o, dx, dg), (want[0], want[2], want[3])):
+        same = (got == ref_)[0].cpu()
+        for c in range(40):
+            bad = seq == touched[c] if c in touched else torch.zeros(170, dtype=torch.bool)
+            assert same[~bad, c].all(), c
+    assert o[0, 60:140, 3].isnan().all() and o[0, 20:40, 5].isinf().all()
+    assert dx[0, 40:91, 7].isnan().all()
+    for got, ref_ in zip((hT, dh0), (want[1], want[4])):
+        same = (got == ref_).cpu()
+        for c in range(40):
+            for n in range(3):
+                assert same[n, c] or touched.get(c) == n
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("B,T,D", [(1, 1, 1), (3, 1, 31), (2, 4, 130), (64, 1, 256), (1, 2, 515)])
+def test_decode(B, T, D, types):
+    for complement in (False, True):
+        v = draw(B, T, D, *types, seed=T + D)
+        o, hT, _, eo, ehT, _ = ref.fwd(np64(v["x"]).reshape(-1, D), np64(v["g"]).reshape(-1, D),
+                                       np64(v["h0"]), ref.segments(B, T), complement)
+        state = v["h0"].cuda()
+        go = gdn.gdn_linrec_decode(v["x"].cuda(), v["g"].cuda(), state, complement=complement)
+        close(go, o, eo, "o")
+        close(state, hT, ehT, "state")
+
+
+def test_prefill_then_decode_carries_the_state():
+    v = draw(2, 303, 96, "fp32", "fp32", seed=12)
+    d = {k: t.cuda() for k, t in v.items()}
+    o, hT, _, eo, ehT, _ = ref.fwd(np64(v["x"]).reshape(-1, 96), np64(v["g"]).reshape(-1, 96),
+                                   np64(v["h0"]), ref.segments(2, 303))
+    o0, h = gdn.gdn_linrec_fwd(d["x"][:, :300].contiguous(), d["g"][:, :300].contiguous(), h0=d["h0"])
+    parts = [o0] + [gdn.gdn_linrec_decode(d["x"][:, t:t + 1].contiguous(),
+                                          d["g"][:, t:t + 1].contiguous(), h) for t in range(300, 303)]
+    close(torch.cat(parts, 1), o.reshape(2, 303, 96), eo.reshape(2, 303, 96), "o")
+    close(h, hT, ehT, "state")
+
+
+def test_gradients_against_differences():
+    """Central differences of sum(do * o) + sum(dhT * hT) in fp64 through the oracle's forward agree
+    with the kernel's gradients (fp32, so to its error bound and the difference's own h^2)."""
+    lengths = [9, 0, 4]
+    v = draw(1, 13, 3, "fp32", "fp32", N=3, seed=21, decay=0.7)
+    x, g, h0, do, dhT = (np64(v[k]).reshape(-1, 3) for k in ("x", "g", "h0", "do", "dhT"))
+    segs = ref.segments(1, 13, [0, 9, 9, 13])
+    for complement in (False, True):
+        def loss(x, g, h0):
+            o, hT = ref.fwd(x, g, h0, segs, complement)[:2]
+            return (do * o).sum() + (dhT * hT).sum()
+
+        got = run_and_check(v, lengths=lengths, complement=complement)[2:]
+        for i, grad in enumerate(got):
+            args = [x, g, h0]
+            for at in np.ndindex(args[i].shape):
+                hi, lo = args[i].copy(), args[i].copy()
+                hi[at] += 1e-5
+                lo[at] -= 1e-5
+                diff = (loss(*[hi if j == i else a for j, a in enumerate(args)]) -
+                        loss(*[lo if j == i else a for j, a in enumerate(args)])) / 2e-5
+                assert abs(np64(grad).reshape(args[i].shape)[at] - diff) <= 1e-5 * (1 + abs(diff))
+
+
+def test_same_results_every_time_and_on_another_stream():
+    v = draw(3, 700, 136, seed=30)
+    first = run_and_check(v)
+    d = {k: t.cuda() for k, t in v.items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        o, hT, states = gdn.gdn_linrec_fwd(d["x"], d["g"], h0=d["h0"], save_states=True, stream=s)
+        grads = gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], h0=d["h0"], dhT=d["dhT"], states=states,
+                                   stream=s)
+        s.synchronize()
+        for a, b in zip((o, hT) + grads, first):
+            assert torch.equal(a, b)
+
+
+def test_captured_calls_replay_on_new_values():
+    """A captured forward and backward without host synchronisation, replayed on other inputs and
+    other document borders (the mirror is only looked at when the call is made)."""
+    lengths = [[100, 50, 150], [10, 0, 290]]
+    v = [draw(1, 300, 64, N=3, seed=s) for s in (1, 2)]
+    want = [run_and_check(a, lengths=b) for a, b in zip(v, lengths)]
+    cu = [torch.tensor([0] + np.cumsum(b).tolist(), dtype=torch.int32) for b in lengths]
+    buf = {k: t.cuda() for k, t in v[0].items()}
+    cu_dev = cu[0].cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kw = dict(cu_seqlens=cu_dev, cu_seqlens_host=cu[0], h0=buf["h0"])
+        out = gdn.gdn_linrec_fwd(buf["x"], buf["g"], **kw)
+        out += gdn.gdn_linrec_bwd(buf["x"], buf["g"], buf["do"], dhT=buf["dhT"], **kw)
+    for i in (0, 1, 0):
+        for k in buf:
+            buf[k].copy_(v[i][k])
+        cu_dev.copy_(cu[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[i]):
+            assert torch.equal(a, b)
+
+
+def test_capture_without_the_host_mirror_is_refused():
+    v = draw(1, 30, 8, N=2)
+    x, g = v["x"].cuda(), v["g"].cuda()
+    cu = torch.tensor([0, 10, 30], dtype=torch.int32, device="cuda")
+    o, hT = gdn.gdn_linrec_fwd(x, g, cu_seqlens=cu)  # without a capture: copied to the host
+    desc = gdn.GdnLinrecDesc(1, 30, 8, 2, 0, 0, 0, 0, 0, gdn.GDN_BF16, gdn.GDN_BF16, 0, 0)
+    import ctypes
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rc = gdn.lib().gdn_linrec_fwd(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), cu.data_ptr(),
+                                      None, None, o.data_ptr(), None, None,
+                                      torch.cuda.current_stream().cuda_stream)
+        o.zero_()
+    assert rc == 1
+
+
+def test_state_offsets_past_32_bits():
+    """More than 2^31 elements of x: the last tokens of a wide, long row."""
+    D, T = 1 << 16, 32784 + 50
+    x = torch.zeros(1, T, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(1, T, D, dtype=torch.bfloat16, device="cuda")
+    x[0, -1] = 1
+    x[0, 5] = 2
+    o, hT = gdn.gdn_linrec_fwd(x, g)
+    assert (o[0, -1] == 3).all() and (o[0, -2] == 2).all() and (o[0, :5] == 0).all()
+    assert (o[0, 5:-1:97] == 2).all() and (hT == 3).all()
+    del o
+    do = torch.zeros_like(x)
+    do[0, -1] = 1
+    dx, dg, dh0 = gdn.gdn_linrec_bwd(x, g, do)
+    assert (dx[0, ::97] == 1).all() and (dg[0, 6:-1:97] == 2).all() and (dh0 == 1).all()
+    assert (dg[0, :6] == 0).all() and (dg[0, -1] == 2).all()
+
+
+def test_planted_launch_failure_is_reported():
+    v = draw(1, 30, 8)
+    x, g, st = v["x"].cuda(), v["g"].cuda(), v["h0"].cuda()
+    gdn.set_test_hook(gdn.GDN_TEST_FAIL_LAUNCH)
+    try:
+        for call in (lambda: gdn.gdn_linrec_fwd(x, g), lambda: gdn.gdn_linrec_bwd(x, g, x),
+                     lambda: gdn.gdn_linrec_decode(x, g, st)):
+            with pytest.raises(gdn.GdnError) as e:
+                call()
+            assert e.value.code == 5
+    finally:
+        gdn.set_test_hook(0)
+    run_and_check(v)
+
+
+def test_launch_trace_names_the_kernels():
+    v = draw(1, 300, 64)
+    d = {k: t.cuda() for k, t in v.items()}
+    with gdn.LaunchTrace(16) as trace:
+        gdn.gdn_linrec_fwd(d["x"], d["g"])
+        gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"])
+        gdn.gdn_linrec_decode(d["x"], d["g"], d["h0"])
+    torch.cuda.synchronize()
+    assert {k: n for k, (n, _) in trace.per_kernel().items()} == {
+        "linrec_fwd": 2, "linrec_bwd": 1, "linrec_decode": 1}
+
+
+def test_empty_rows_pass_the_states_through():
+    x = torch.zeros(1, 0, 40, dtype=torch.bfloat16, device="cuda")
+    h0, dhT = torch.randn(3, 40, device="cuda"), torch.randn(3, 40, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32)
+    o, hT = gdn.gdn_linrec_fwd(x, x, cu_seqlens=cu.cuda(), cu_seqlens_host=cu, h0=h0)
+    assert o.shape == x.shape and torch.equal(hT, h0)
+    dh0 = gdn.gdn_linrec_bwd(x, x, x, cu_seqlens=cu.cuda(), cu_seqlens_host=cu, dhT=dhT)[2]
+    assert torch.equal(dh0, dhT)
