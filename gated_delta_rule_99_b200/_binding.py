@@ -23,7 +23,8 @@ EXPORTS = ("gdn_version", "gdn_chunk_size", "gdn_fwd_workspace_size", "gdn_bwd_w
            "gdn_fwd", "gdn_fwd_noalloc", "gdn_fwd_noalloc_status", "gdn_bwd", "gdn_decode",
            "gdn_device_status", "gdn_status_string", "gdn_trace_install", "gdn_kernel_name",
            "gdn_set_wait_limit", "gdn_set_test_hook", "gdn_linrec_states_size", "gdn_linrec_fwd",
-           "gdn_linrec_bwd", "gdn_linrec_decode")
+           "gdn_linrec_bwd", "gdn_linrec_decode", "gdn_qk_norm_rope_fwd",
+           "gdn_qk_norm_rope_bwd_workspace_size", "gdn_qk_norm_rope_bwd")
 GDN_TEST_STALL_COPY, GDN_TEST_FAIL_LAUNCH = 1, 2
 
 
@@ -43,12 +44,21 @@ GDN_FLAG_PIECE_SCAN = 1
 GDN_FLAG_QK_L2NORM = 2
 GDN_FLAG_VALUE_SLICES = 4
 GDN_LINREC_COMPLEMENT = 1
+GDN_NORM_NONE, GDN_NORM_L2, GDN_NORM_RMS = 0, 1, 2
+GDN_QK_INTERLEAVED = 1
 
 
 class GdnLinrecDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "D", "n_seqs", "x_stride", "g_stride",
                                               "o_stride", "dx_stride", "dg_stride")] + \
                [(n, ctypes.c_int32) for n in ("dtype", "g_dtype", "flags", "reserved")]
+
+
+class GdnQkDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hk", "d", "rot", "q_stride",
+                                              "k_stride", "qo_stride", "ko_stride", "dq_stride",
+                                              "dk_stride")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "norm", "flags")] + [("eps", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -95,6 +105,14 @@ def lib() -> ctypes.CDLL:
                                          sz, vp]
             L.gdn_linrec_decode.restype = ctypes.c_int
             L.gdn_linrec_decode.argtypes = [lp, vp, vp, fp, vp, vp]
+            qp = ctypes.POINTER(GdnQkDesc)
+            L.gdn_qk_norm_rope_fwd.restype = ctypes.c_int
+            L.gdn_qk_norm_rope_fwd.argtypes = [qp, vp, vp, i32p, fp, fp, fp, vp, vp, vp]
+            L.gdn_qk_norm_rope_bwd_workspace_size.restype = sz
+            L.gdn_qk_norm_rope_bwd_workspace_size.argtypes = [qp]
+            L.gdn_qk_norm_rope_bwd.restype = ctypes.c_int
+            L.gdn_qk_norm_rope_bwd.argtypes = [qp, vp, vp, i32p, fp, fp, fp, vp, vp, vp, vp, fp, fp,
+                                               vp, sz, vp]
             L.gdn_device_status.restype = ctypes.c_int
             L.gdn_device_status.argtypes = [vp, vp]
             L.gdn_status_string.restype = ctypes.c_char_p
@@ -440,6 +458,102 @@ def gdn_linrec_decode(x, g, state, complement=False, o=None, stream=None):
     if rc:
         raise GdnError(rc, "gdn_linrec_decode")
     return o
+
+
+# ------------------------------------------- q/k normalisation with the position rotation
+_NORMS = {None: (GDN_NORM_NONE, 0.0), "l2": (GDN_NORM_L2, 0.0), "rms": (GDN_NORM_RMS, 1e-6)}
+
+
+def _qk_call(q, k, inv_freq, positions, norm, q_weight, k_weight, eps, interleaved, outs, raws):
+    """Checks of the arguments both passes share, and the descriptor.  outs: the rotated q and k
+    or their gradients, raws: the gradients of the raw q and k (None where not given)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must have shape (B, T, heads, d)")
+    if q.dtype not in _DT:
+        raise ValueError("q must be bf16 or fp32")
+    if norm not in _NORMS:
+        raise ValueError("norm must be None, 'l2' or 'rms', got %r" % (norm,))
+    dev = q.device
+    B, T, Hq, d = q.shape
+    Hk = k.shape[2]
+    shapes = ((B, T, Hq, d), (B, T, Hk, d))
+    row = lambda t, name, i: 0 if t is None else _row_stride(t, name, dev, q.dtype, shapes[i])
+    _check_on(inv_freq, "inv_freq", dev, torch.float32)
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
+    _check_on(positions, "positions", dev, torch.int32, (B, T))
+    _check_on(q_weight, "q_weight", dev, torch.float32, (d,))
+    _check_on(k_weight, "k_weight", dev, torch.float32, (d,))
+    code, default = _NORMS[norm]
+    return GdnQkDesc(B, T, Hq, Hk, d, 0 if inv_freq is None else 2 * inv_freq.numel(),
+                     row(q, "q", 0), row(k, "k", 1), row(outs[0], "qo", 0), row(outs[1], "ko", 1),
+                     row(raws[0], "dq", 0), row(raws[1], "dk", 1), _DT[q.dtype], code,
+                     GDN_QK_INTERLEAVED if interleaved else 0, default if eps is None else eps)
+
+
+def gdn_qk_norm_rope_fwd(q, k, inv_freq=None, positions=None, norm="rms", q_weight=None,
+                         k_weight=None, eps=None, interleaved=False, qo=None, ko=None,
+                         stream=None):
+    """Rows of q (B, T, Hq, d) and k (B, T, Hk, d) normalised (``norm``: "rms", "l2" or None),
+    multiplied by the weights (d,) fp32, and turned by the angles positions x inv_freq
+    (positions: (B, T) int32, or None to count along each row; inv_freq: (rot/2,) fp32, or None
+    for no rotation), through the C ABI.  eps defaults to 1e-6 for "rms" and 0 for "l2".
+    Returns (qo, ko)."""
+    L = lib()
+    dev = q.device
+    scope, stream = _scope(dev, stream, (q, k, inv_freq, positions, q_weight, k_weight, qo, ko))
+    with scope:
+        desc = _qk_call(q, k, inv_freq, positions, norm, q_weight, k_weight, eps, interleaved,
+                        (qo, ko), (None, None))
+        if qo is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if ko is None:
+            ko = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        rc = L.gdn_qk_norm_rope_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(),
+                                    _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
+                                    _ptr(k_weight), qo.data_ptr(), ko.data_ptr(),
+                                    stream.cuda_stream)
+    if rc:
+        raise GdnError(rc, "gdn_qk_norm_rope_fwd")
+    return qo, ko
+
+
+def gdn_qk_norm_rope_bwd(q, k, dqo, dko, inv_freq=None, positions=None, norm="rms",
+                         q_weight=None, k_weight=None, eps=None, interleaved=False, grads=None,
+                         workspace=None, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of gdn_qk_norm_rope_fwd for upstream dqo, dko,
+    through the C ABI; a weight that is None has no gradient (None)."""
+    L = lib()
+    dev = q.device
+    dq, dk, dqw, dkw = grads if grads is not None else (None, None, None, None)
+    scope, stream = _scope(dev, stream, (q, k, dqo, dko, inv_freq, positions, q_weight, k_weight,
+                                         dq, dk, dqw, dkw, workspace))
+    with scope:
+        desc = _qk_call(q, k, inv_freq, positions, norm, q_weight, k_weight, eps, interleaved,
+                        (dqo, dko), (dq, dk))
+        d = (q.shape[3],)
+        _check_on(dqw, "dq_weight", dev, torch.float32, d)
+        _check_on(dkw, "dk_weight", dev, torch.float32, d)
+        _check_on(workspace, "workspace", dev, torch.uint8)
+        if grads is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+            dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+        if workspace is None and (dqw is not None or dkw is not None):
+            need = L.gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(desc))
+            if need == 0:
+                raise GdnError(2, "gdn_qk_norm_rope_bwd_workspace_size")
+            workspace = alloc_workspace(need, dev)
+        rc = L.gdn_qk_norm_rope_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(),
+                                    _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
+                                    _ptr(k_weight), dqo.data_ptr(), dko.data_ptr(), _ptr(dq),
+                                    _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace),
+                                    0 if workspace is None else workspace.numel(),
+                                    stream.cuda_stream)
+    if rc:
+        raise GdnError(rc, "gdn_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
 
 
 def device_status(workspace, stream=None) -> int:

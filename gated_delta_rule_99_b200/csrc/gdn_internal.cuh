@@ -185,6 +185,9 @@ enum KernelId : int32_t {
     kKLinrecFwd,
     kKLinrecBwd,
     kKLinrecDecode,
+    kKQkRope,
+    kKQkRopeBwd,
+    kKQkRopeDw,
     kKernelCount
 };
 

@@ -275,6 +275,69 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void
 gdn_status gdn_linrec_decode(const gdn_linrec_desc *desc, const void *x, const void *g,
                              float *state, void *o, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Normalisation of q and k per token and head with the position rotation, in
+ * one pass: the q and k that gdn_fwd and gdn_decode take.  For every row x of d
+ * values (one token and head),
+ *
+ *     y = R(p) (w x r),   r = 1 / sqrt(c |x|^2 + eps)   (0 where that sum is 0)
+ *     c = 1 (GDN_NORM_L2, as GDN_FLAG_QK_L2NORM with eps = 0), 1/d (GDN_NORM_RMS);
+ *     r = 1 with GDN_NORM_NONE
+ *
+ * with w = q_weight or k_weight (d fp32 values; NULL: ones), and R(p) turning
+ * the pairs of the row's first `rot` values by the angles p inv_freq[i],
+ * i < rot / 2: (a, b) -> (a cos - b sin, a sin + b cos).  Pair i is the values i
+ * and i + rot / 2, or 2 i and 2 i + 1 with GDN_QK_INTERLEAVED; values from rot on
+ * are not turned.  p is the token's position (int32, any sign), or its index in
+ * its row with positions NULL; the angle is formed and reduced in 64 bits, so
+ * far positions are exact.  Norms and rotations are in fp32, rounded once to dtype.
+ * |x|^2 is an fp32 sum: a row whose sum underflows to 0 counts as a zero row.
+ *
+ * Layouts: q, qo, dqo, dq [B][T][Hq][d] and k, ko, dko, dk [B][T][Hk][d] in
+ * dtype, a token's heads adjacent; the strides give the elements from one token
+ * to the next (0: H * d), so that q and k can be column slices of one
+ * projection.  These pointers are 16-byte aligned; positions [B][T], inv_freq
+ * [rot / 2] (fp32, may be NULL with rot = 0) and the weights 4-byte aligned.
+ * Outputs must not overlap inputs.  No address depends on the values of positions. */
+#define GDN_NORM_NONE 0
+#define GDN_NORM_L2 1
+#define GDN_NORM_RMS 2
+#define GDN_QK_INTERLEAVED 1
+
+typedef struct gdn_qk_desc {
+    int64_t B, T;    /* rows and tokens per row; B * T < 2^31 */
+    int64_t Hq, Hk;  /* heads of q and of k, 1 .. 65535 */
+    int64_t d;       /* values per row: even, 2 .. 256 */
+    int64_t rot;     /* values that are rotated: even, 0 .. d */
+    int64_t q_stride, k_stride;   /* of q, k;                 0 = H * d */
+    int64_t qo_stride, ko_stride; /* of qo, ko, or dqo, dko;  0 = H * d */
+    int64_t dq_stride, dk_stride; /* of dq, dk;               0 = H * d */
+    int32_t dtype;   /* gdn_dtype */
+    int32_t norm;    /* GDN_NORM_* */
+    int32_t flags;   /* GDN_QK_INTERLEAVED or 0 */
+    float eps;       /* >= 0, finite */
+} gdn_qk_desc;
+
+gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_desc *desc, const void *q, const void *k,
+                                const int32_t *positions, const float *inv_freq,
+                                const float *q_weight, const float *k_weight, void *qo, void *ko,
+                                void *stream);
+
+/* Workspace of the backward: partial sums of the weights' gradients (depends only
+ * on the descriptor; 0 on a bad one). */
+size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_desc *desc);
+
+/* Backward: from the raw q and k and the gradients dqo, dko of qo, ko,
+ *     u = R(p)^T dy,   dx = r (w u - c (x r) <w u, x r>),   dw = sum of u x r over rows
+ * dq_weight, dk_weight (d fp32 values each, overwritten) are written where they are
+ * not NULL; the workspace is needed (256-byte aligned) where one of them is. */
+gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_desc *desc, const void *q, const void *k,
+                                const int32_t *positions, const float *inv_freq,
+                                const float *q_weight, const float *k_weight, const void *dqo,
+                                const void *dko, void *dq, void *dk, float *dq_weight,
+                                float *dk_weight, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
 /* Synchronises the stream, then returns and clears the device-side status
  * that the last gdn_fwd/gdn_bwd on this workspace recorded (GDN_OK,
  * GDN_ERR_TIMEOUT, or GDN_ERR_INVALID_ARG when the device copy of cu_seqlens
