@@ -208,7 +208,7 @@ gdn_status gdn_decode(const gdn_desc *desc, const void *q, const void *k, const 
  *
  * g is the log-decay, one value per token and channel (g <= 0 in use; -inf is
  * a reset to w_t x_t; a positive g grows the state, and the products of the
- * factors over up to 1024 tokens then have to stay below the fp32 maximum).
+ * factors over up to 64 tokens then have to stay below the fp32 maximum).
  * A NaN or infinity stays in its channel and its sequence.
  *
  * Layouts: x, o, do_, dx [B][T][D] in dtype; g, dg [B][T][D] in g_dtype
@@ -246,7 +246,7 @@ typedef struct gdn_linrec_desc {
 } gdn_linrec_desc;
 
 /* Bytes of the `states` buffer that the forward can leave for the backward
- * (the fp32 states entering every 128th token: 1/32 float per element), which
+ * (the fp32 states entering every 64th token, 1/16 byte per element), which
  * is also the backward's workspace size (0 on a bad descriptor). */
 size_t gdn_linrec_states_size(const gdn_linrec_desc *desc);
 

@@ -144,7 +144,7 @@ def test_states_size_counts_every_tile():
     size = lambda **kw: gdn.lib().gdn_linrec_states_size(ctypes.byref(desc(**kw)))
     assert size(B=1, T=0) == 256
     for B, T, D in ((1, 4096, 2048), (3, 1237, 515), (1, 1 << 20, 1024), (1024, 8, 64)):
-        tiles = -(-T // 128) * B if T > 128 else 0  # a shorter row starts within its tile
+        tiles = -(-T // 64) * B if T > 64 else 0  # a shorter row starts within its tile
         assert size(B=B, T=T, D=D) >= 4 * D * tiles
 
 
