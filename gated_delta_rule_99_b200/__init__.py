@@ -11,11 +11,12 @@ from ._binding import (EXPORTS, GDN_BF16, GDN_FLAG_PIECE_SCAN, GDN_FLAG_QK_L2NOR
                        GDN_TEST_FAIL_LAUNCH, GDN_TEST_STALL_COPY, GdnDesc, GdnError, GdnLinrecDesc, GdnQkDesc, LaunchTrace,
                        alloc_workspace, bwd_workspace_size, device_status, fwd_workspace_size,
                        gdn_bwd, gdn_decode, gdn_fwd, gdn_linrec_bwd, gdn_linrec_decode,
-                       gdn_linrec_fwd, gdn_qk_norm_rope_bwd, gdn_qk_norm_rope_fwd, lib, make_desc, set_test_hook,
+                       gdn_linrec_fwd, gdn_qk_norm_rope_bwd, gdn_qk_norm_rope_fwd, lib,
+                       linrec_status, make_desc, set_test_hook,
                        set_wait_limit)
 
 __all__ = ["gdn_fwd", "gdn_bwd", "gdn_decode", "gdn_linrec_fwd", "gdn_linrec_bwd",
-           "gdn_linrec_decode", "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd", "device_status", "fwd_workspace_size",
+           "gdn_linrec_decode", "linrec_status", "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd", "device_status", "fwd_workspace_size",
            "bwd_workspace_size", "alloc_workspace", "LaunchTrace", "make_desc", "GdnDesc",
            "GdnError", "lib", "GDN_BF16", "GDN_FP32", "GDN_FLAG_PIECE_SCAN", "GDN_FLAG_QK_L2NORM",
            "GDN_FLAG_VALUE_SLICES", "GDN_LINREC_COMPLEMENT", "GdnLinrecDesc", "GDN_NORM_NONE",

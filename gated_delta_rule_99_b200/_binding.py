@@ -22,7 +22,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "mi
 EXPORTS = ("gdn_version", "gdn_chunk_size", "gdn_fwd_workspace_size", "gdn_bwd_workspace_size",
            "gdn_fwd", "gdn_fwd_noalloc", "gdn_fwd_noalloc_status", "gdn_bwd", "gdn_decode",
            "gdn_device_status", "gdn_status_string", "gdn_trace_install", "gdn_kernel_name",
-           "gdn_set_wait_limit", "gdn_set_test_hook", "gdn_linrec_states_size", "gdn_linrec_fwd",
+           "gdn_set_wait_limit", "gdn_set_test_hook", "gdn_linrec_states_size", "gdn_linrec_fwd", "gdn_linrec_status",
            "gdn_linrec_bwd", "gdn_linrec_decode", "gdn_qk_norm_rope_fwd",
            "gdn_qk_norm_rope_bwd_workspace_size", "gdn_qk_norm_rope_bwd")
 GDN_TEST_STALL_COPY, GDN_TEST_FAIL_LAUNCH = 1, 2
@@ -103,6 +103,8 @@ def lib() -> ctypes.CDLL:
             L.gdn_linrec_bwd.restype = ctypes.c_int
             L.gdn_linrec_bwd.argtypes = [lp, vp, vp, i32p, i32p, fp, vp, fp, vp, vp, fp, fp, vp,
                                          sz, vp]
+            L.gdn_linrec_status.restype = ctypes.c_int
+            L.gdn_linrec_status.argtypes = [vp]
             L.gdn_linrec_decode.restype = ctypes.c_int
             L.gdn_linrec_decode.argtypes = [lp, vp, vp, fp, vp, vp]
             qp = ctypes.POINTER(GdnQkDesc)
@@ -440,6 +442,12 @@ def gdn_linrec_bwd(x, g, do, cu_seqlens=None, h0=None, dhT=None, complement=Fals
     if rc:
         raise GdnError(rc, "gdn_linrec_bwd")
     return dx, dg, dh0
+
+
+def linrec_status(stream=None) -> int:
+    """Status code of this device's gdn_linrec_fwd and gdn_linrec_bwd calls (0: ok), after
+    waiting for the stream; reading clears it."""
+    return int(lib().gdn_linrec_status(_stream(stream)))
 
 
 def gdn_linrec_decode(x, g, state, complement=False, o=None, stream=None):

@@ -4,15 +4,17 @@
 // A sequence's map over any span of tokens is affine per channel, h' = A h + X with
 // A the product of the span's factors, and the reverse map of the gradients is
 // r' = A r + Y with the same A; spans join by (A2, X2)(A1, X1) = (A2 A1, A2 X1 + X2).
-// So a CTA takes 64 channels (two per lane) and 64 tokens at a time, 8 tokens per warp in
-// registers: each warp forms its span's A and X (and Y), the 8 spans are joined in
-// shared memory, and the warp then runs its tokens from the state that enters them.  A
-// cluster of up to 16 CTAs takes consecutive tiles of the same channels and joins the
-// tiles' maps over distributed shared memory, one cluster barrier per step; every CTA
-// folds all of them, so each keeps the state that enters the next step.  Joins go in
-// token order from the state itself, so results do not depend on the cluster's size or
-// on timing.  The data is read once: the next steps' tiles are already on their way by
-// cp.async, each warp copying the rows it will use.
+// A CTA takes 64 channels (two per lane) and a tile of tokens at a time, split into one
+// span per warp, whose tokens stay in registers.  Each of eight warps forms its span's A
+// and X (and Y) and joins the spans before it; the last one, which thereby has the tile's
+// map, carries the state.  A cluster of up to 16 CTAs takes consecutive tiles of the same
+// channels: the carrying warps send their tile's map to all of them (st.async into
+// distributed shared memory, counted by an mbarrier: no cluster barrier, whose release
+// would wait for the outputs still being stored) and each folds them in order, so each holds
+// the state that enters its tile and the next step.  Joins go in token order and tile by
+// tile, so results depend neither on the cluster's size nor on timing.  The data is read
+// once: the next steps' tiles are on their way by cp.async, each warp copying the rows
+// that it will use.
 //
 // A start of a sequence inside a span drops what comes before it by selection (not by a
 // factor of 0), so that no infinity or NaN crosses; padded tokens are zeros (factor
@@ -25,24 +27,29 @@
 #include <vector>
 
 #include "gdn_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kSpan = 8;               // tokens per warp
 constexpr int kWarps = 8;
-constexpr int kTile = kSpan * kWarps;  // tokens per CTA and step, and between saved states
+constexpr int kThreads = 32 * kWarps;
 constexpr int kCh = 64;                // channels per CTA
+constexpr int kSaved = 64;             // tokens between two saved states
+constexpr int kMaxSpan = 16;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 16;
 constexpr int kSms = 148, kPerSm = 2;
-constexpr size_t kSmemSm = 227 * 1024, kSmemMax = 196 * 1024, kSmemStatic = 31 * 1024;  // dynamic, static and reserved
+constexpr size_t kSmemSm = 227 * 1024, kSmemMax = 200 * 1024, kSmemStatic = 25 * 1024;  // dynamic, static and reserved
 
 struct LinrecParams {
     int64_t T, BT, D, N;
     int64_t xs, gs, os, dxs, dgs;
-    int64_t streams, rows_per_stream, tiles;  // a stream: one dense row, several short ones, or the packed row
+    int64_t streams, rows_per_stream;  // a stream: one dense row, several short ones, or the packed row
+    int64_t saved;                            // saved states of a stream
     int32_t slabs, cluster, stages, wide, even;
+    uint32_t wait_limit;
+    int32_t test_hook;
     const int32_t *cu;
     const void *x, *g, *dy;
     const float *h0, *dhT;
@@ -84,16 +91,49 @@ __device__ __forceinline__ void store_state(float *p, int64_t at, float2 v, int 
     if (p && n > 0) p[at] = v.x;
     if (p && n > 1) p[at + 1] = v.y;
 }
+// Two lanes' worth of fp32 arithmetic per instruction.
+__device__ __forceinline__ uint64_t bits(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
+__device__ __forceinline__ float2 pair(uint64_t b) { return *reinterpret_cast<float2 *>(&b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(d);
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// a = exp(g), and the write strength 1 or 1 - a; the latter without the cancellation.
-template <bool COMP>
-__device__ __forceinline__ void gate(float2 g, float2 *a, float2 *w) {
-    *a = make_float2(__expf(g.x), __expf(g.y));
-    *w = COMP ? make_float2(-expm1f(g.x), -expm1f(g.y)) : make_float2(1.f, 1.f);
+__device__ __forceinline__ float exp_base2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// a = exp(g), to 2 ulp and the rounding of g log2(e).
+__device__ __forceinline__ float2 decay(float2 g) {
+    const float2 e = mul2(g, both(1.44269504088896341f));
+    return make_float2(exp_base2(e.x), exp_base2(e.y));
+}
+// 1 - a without its cancellation: for |g| <= 1/2 the Taylor polynomial of 1 - exp(g) to g^8
+// (the next term is below 2^-26 of the sum), beyond it the difference.
+__device__ __forceinline__ float2 strength(float2 g, float2 a) {
+    float2 s = both(-1.f / 40320);
+    s = fma2(s, g, both(-1.f / 5040));
+    s = fma2(s, g, both(-1.f / 720));
+    s = fma2(s, g, both(-1.f / 120));
+    s = fma2(s, g, both(-1.f / 24));
+    s = fma2(s, g, both(-1.f / 6));
+    s = fma2(s, g, both(-1.f / 2));
+    s = fma2(s, g, both(-1.f));
+    s = mul2(s, g);
+    return make_float2(fabsf(g.x) <= 0.5f ? s.x : 1.f - a.x, fabsf(g.y) <= 0.5f ? s.y : 1.f - a.y);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -121,10 +161,10 @@ __device__ __forceinline__ void copy_wait(int pending) {
     }
 }
 
-// A warp's copy of 8 tokens x 64 channels; `rows` and `cols` of them exist, the rest become
+// A warp's copy of its span's tokens x 64 channels; `rows` and `cols` of them exist, the rest become
 // zeros.  wide: 16-byte pieces (rows 16-byte aligned; the last piece may be partial), else 4
 // bytes (fp32, or bf16 with even rows), else one bf16 after another.
-template <typename E>
+template <int kSpan, typename E>
 __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, int rows, int cols,
                                           int wide, int even, int lane) {
     if (wide) {
@@ -146,36 +186,42 @@ __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, 
                 copy_async<4>(dst + r * kCh + c, in ? src + r * stride + c : src, in ? 4 : 0);
             }
     } else {
-        E v[kSpan][2];
+#pragma unroll 1
+        for (int i = 0; i < kSpan; i += 4) {
+            E v[4][2];
 #pragma unroll
-        for (int r = 0; r < kSpan; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = lane + 32 * j;
-                v[r][j] = r < rows && c < cols ? src[r * stride + c] : E(0.f);
-            }
+                for (int j = 0; j < 2; ++j) {
+                    const int c = lane + 32 * j;
+                    v[r][j] = i + r < rows && c < cols ? src[(i + r) * stride + c] : E(0.f);
+                }
 #pragma unroll
-        for (int r = 0; r < kSpan; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) dst[r * kCh + lane + 32 * j] = v[r][j];
+                for (int j = 0; j < 2; ++j) dst[(i + r) * kCh + lane + 32 * j] = v[r][j];
+        }
     }
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void cluster_store(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+// Asynchronous stores into a CTA of the cluster; their bytes count down its mbarrier.
+__device__ __forceinline__ void send(uint32_t addr, float4 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void cluster_store(uint32_t addr, int v) {
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void send(uint32_t addr, int v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];"
+                 ::"r"(addr), "r"(v), "r"(bar) : "memory");
 }
+constexpr uint32_t kMapBytes = 32 * 16 + 4;  // a tile's map and its cut flag
+
+// Status of this device's calls (gdn_linrec_status).
+__device__ int32_t g_status;
 
 // ---------------------------------------------------------------- sequences of a stream
 // The sequence that holds a token, for a whole warp: index n, tokens [beg, end) of the stream.
@@ -261,13 +307,13 @@ __device__ __forceinline__ Marks mark(const LinrecParams &p, int64_t first, int 
 struct Unit {
     int64_t first;  // first sequence of the stream (dense)
     int64_t tok0;   // the stream's first token
-    int64_t tile0;  // its first saved state
+    int64_t saved0; // its first saved state
     int S, steps;   // its tokens, and the cluster's steps over them
     int64_t c0;
     int cols, mine;  // channels of the CTA, and of this lane (0, 1 or 2)
     int rank;
 };
-__device__ __forceinline__ Unit unit_of(const LinrecParams &p, int lane) {
+__device__ __forceinline__ Unit unit_of(const LinrecParams &p, int tile, int lane) {
     Unit u;
     u.rank = blockIdx.x % p.cluster;
     const int64_t i = blockIdx.x / p.cluster, stream = i / p.slabs;
@@ -284,8 +330,8 @@ __device__ __forceinline__ Unit unit_of(const LinrecParams &p, int lane) {
         u.tok0 = u.first * p.T;
         u.S = (int)(rows * p.T);
     }
-    u.tile0 = stream * p.tiles;
-    u.steps = (int)((u.S + (int64_t)kTile * p.cluster - 1) / ((int64_t)kTile * p.cluster));
+    u.saved0 = stream * p.saved;
+    u.steps = (int)((u.S + (int64_t)tile * p.cluster - 1) / ((int64_t)tile * p.cluster));
     return u;
 }
 
@@ -305,127 +351,302 @@ __device__ __forceinline__ void pass_empty(const LinrecParams &p, const Unit &u,
     }
 }
 
-// ---------------------------------------------------------------- forward
-template <typename T, typename G, bool COMP, bool EVEN>
-__global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float4 spans[2][kWarps][32], tiles[2][kMaxCluster][32];  // (A, X) of two channels
-    __shared__ int span_cut[2][kWarps], tile_cut[2][kMaxCluster];       // 1: what comes before does not count
-    __shared__ int start_of[kWarps][kSpan], end_of[kWarps][kSpan];
-    constexpr int kRowsX = kSpan * kCh * sizeof(T), kRows = kRowsX + kSpan * kCh * sizeof(G);
+// ---------------------------------------------------------------- the carrying warp
+// Shared memory of a CTA.
+struct Shared {
+    float4 spans[kWarps][32];               // a span's map (A, X) of the lane's two channels; backward: (A, Y)
+    float2 starts[kWarps][32];              // backward: X
+    float4 maps[2][kMaxCluster][32];        // the cluster's tiles' maps
+    float2 enter[32];                       // what enters the CTA's tile
+    uint64_t bar[2];                        // arrivals of maps[0], maps[1]
+    int map_cut[2][kMaxCluster];
+    int cut[kWarps];                        // bit 0: a start in the span, bit 1: an end
+    int start_of[2][kWarps][kMaxSpan], end_of[2][kWarps][kMaxSpan];
+    int dead;                               // a wait ran out
+};
 
+__device__ __forceinline__ float2 join(float4 s, bool cut, float2 h) {
+    return cut ? make_float2(s.y, s.w) : fma2(make_float2(s.x, s.z), h, make_float2(s.y, s.w));
+}
+
+// Waits (up to `limit` polls) for the phase of this parity: all maps are here.
+__device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred q;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if (i > 64) __nanosleep(32);
+    }
+    return false;
+}
+
+// Makes the mbarriers ready in every CTA of the cluster before anyone sends.
+__device__ __forceinline__ void cluster_begin(Shared &sh, int cluster) {
+    if (threadIdx.x == 0) {
+        sh.dead = 0;
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.bar[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (cluster > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+__device__ __forceinline__ void cluster_ready(int cluster) {
+    if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// No CTA leaves while another may still send to it.
+__device__ __forceinline__ void cluster_end(int cluster) {
+    if (cluster > 1) {
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    }
+}
+
+// The carrying warp's part of a step, between the CTA's two barriers: sends the tile's map q to
+// the cluster, forms what enters the tile from all tiles of the step, and the new carry.  REV:
+// from the last rank to the first.
+__device__ __forceinline__ void send_map(const LinrecParams &p, Shared &sh, int rank, int step, int lane, float4 q, bool cut) {
+    if (p.cluster == 1) return;
+    const int buf = step & 1;
+    if (lane == 0) {
+        const bool stall = p.test_hook == GDN_TEST_STALL_COPY && blockIdx.x == 0 && step == 0;
+        ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * kMapBytes + (stall ? 16 : 0));
+    }
+    for (int r = 0; r < p.cluster; ++r) {
+        const uint32_t bar = cluster_addr(&sh.bar[buf], r);
+        send(cluster_addr(&sh.maps[buf][rank][lane], r), q, bar);
+        if (lane == 0) send(cluster_addr(&sh.map_cut[buf][rank], r), cut, bar);
+    }
+}
+template <bool REV>
+__device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, int rank, int step, int lane, float4 q, bool cut, float2 *carry) {
+    if (p.cluster == 1) {
+        sh.enter[lane] = *carry;
+        *carry = join(q, cut, *carry);
+        return;
+    }
+    const int buf = step & 1;
+    if (!__all_sync(0xffffffffu, arrived(&sh.bar[buf], (step >> 1) & 1, p.wait_limit))) {
+        if (lane == 0) {
+            sh.dead = 1;
+            g_status = kDevTimeout;
+        }
+        return;
+    }
+    float2 c = *carry;
+    for (int i = 0; i < p.cluster; ++i) {
+        const int j = REV ? p.cluster - 1 - i : i;
+        if (j == rank) sh.enter[lane] = c;
+        c = join(sh.maps[buf][j][lane], sh.map_cut[buf][j], c);
+    }
+    *carry = c;
+}
+
+// ---------------------------------------------------------------- forward
+// PLAIN: no sequence starts or ends among the span's tokens, and none is missing.
+template <bool PLAIN, int kSpan>
+__device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                           const float2 (&v)[kSpan], uint32_t starts, const int *start_of, int64_t c) {
+    float2 A = a[0], X = v[0];
+    if (!PLAIN && (starts & 1)) X = fma2(a[0], load_state(p.h0, start_of[0] * p.D + c, u.mine), v[0]);
+#pragma unroll
+    for (int i = 1; i < kSpan; ++i) {
+        if (!PLAIN && (starts >> i & 1)) X = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        X = fma2(a[i], X, v[i]);
+        A = mul2(A, a[i]);
+    }
+    return make_float4(A.x, X.x, A.y, X.y);
+}
+
+template <bool PLAIN, bool EVEN, int kSpan, typename T>
+__device__ __forceinline__ void run_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                         const float2 (&v)[kSpan], float2 h, Marks m, int count,
+                                         const int *start_of, const int *end_of, int64_t c, T *o) {
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+        if (!PLAIN && (m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        h = fma2(a[i], h, v[i]);
+        if (o && (PLAIN || i < count)) store_pair<EVEN>(o + i * p.os, h, u.mine);
+        if (!PLAIN && (m.ends >> i & 1)) store_state(p.hT, end_of[i] * p.D + c, h, u.mine);
+    }
+}
+
+template <int kSpan, typename T, typename G, bool COMP, bool EVEN>
+__global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Shared sh;
+    constexpr int kTile = kSpan * kWarps;
+    constexpr int kRowsX = kSpan * kCh * sizeof(T), kRows = kRowsX + kSpan * kCh * sizeof(G);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, stages = p.stages;
-    const Unit u = unit_of(p, lane);
+    const Unit u = unit_of(p, kTile, lane);
+    const int64_t c = u.c0 + 2 * lane;
+    cluster_begin(sh, cluster);
+
     unsigned char *mine = smem + (size_t)warp * stages * kRows;
     const T *x = static_cast<const T *>(p.x) + u.tok0 * p.xs + u.c0;
     const G *g = static_cast<const G *>(p.g) + u.tok0 * p.gs + u.c0;
-    T *o = static_cast<T *>(p.o);
-    if (o) o += u.tok0 * p.os + u.c0 + 2 * lane;
-    const auto first_token = [&](int step) { return (int64_t)(step * (int64_t)cluster + u.rank) * kTile + warp * kSpan; };
+    T *o = p.o ? static_cast<T *>(p.o) + u.tok0 * p.os + c : nullptr;
+    const auto first_token = [&](int step) { return ((int64_t)step * cluster + u.rank) * kTile + warp * kSpan; };
     const auto fetch = [&](int step, int stage) {
         const int64_t t0 = first_token(step);
         if (step < u.steps) {
             const int rows = t0 >= u.S ? 0 : u.S - t0 < kSpan ? (int)(u.S - t0) : kSpan;
             unsigned char *to = mine + stage * kRows;
-            copy_rows(reinterpret_cast<T *>(to), rows ? x + t0 * p.xs : x, p.xs, rows, u.cols, p.wide, p.even, lane);
-            copy_rows(reinterpret_cast<G *>(to + kRowsX), rows ? g + t0 * p.gs : g, p.gs, rows, u.cols, p.wide, p.even, lane);
+            copy_rows<kSpan>(reinterpret_cast<T *>(to), rows ? x + t0 * p.xs : x, p.xs, rows, u.cols, p.wide, p.even, lane);
+            copy_rows<kSpan>(reinterpret_cast<G *>(to + kRowsX), rows ? g + t0 * p.gs : g, p.gs, rows, u.cols, p.wide, p.even, lane);
         }
         copy_commit();
     };
-    for (int i = 0; i < stages; ++i) fetch(i, i);
-    if (cluster > 1) cluster_sync();  // the others run: their shared memory may be written
-
     Seq seq = {0, 0, 0};
-    float2 carry = make_float2(0.f, 0.f);  // the state that enters the cluster's step
-    for (int step = 0, stage = 0; step < u.steps; ++step, stage = stage + 1 == stages ? 0 : stage + 1) {
-        const int buf = step & 1;
+    const auto marks = [&](int step) {
         const int64_t at = first_token(step);
         const int t0 = at < u.S ? (int)at : u.S, t1 = u.S - t0 < kSpan ? u.S : t0 + kSpan;
-        __syncwarp();
-        const Marks m = mark(p, u.first, u.S, t0, t1, lane, &seq, start_of[warp], end_of[warp]);
+        return step < u.steps ? mark(p, u.first, u.S, t0, t1, lane, &seq, sh.start_of[step & 1][warp], sh.end_of[step & 1][warp]) : Marks{0, 0};
+    };
+    for (int i = 0; i < stages; ++i) fetch(i, i);
+    Marks next = marks(0);
+    float2 carry = both(0.f);  // the state that enters the cluster's step (the last warp's)
+    cluster_ready(cluster);
+
+    for (int step = 0, stage = 0; step < u.steps; ++step, stage = stage + 1 == stages ? 0 : stage + 1) {
+        const Marks m = next;
+        const int *start_of = sh.start_of[step & 1][warp], *end_of = sh.end_of[step & 1][warp];
+        const int64_t at = first_token(step);
+        const int count = at >= u.S ? 0 : u.S - at < kSpan ? (int)(u.S - at) : kSpan;
+        const bool plain = !(m.starts | m.ends) && count == kSpan;
         copy_wait(stages - 1);
         __syncwarp();
-        // the span's map
-        float2 a[kSpan], v[kSpan], A = make_float2(1.f, 1.f), X = make_float2(0.f, 0.f);
+        float2 a[kSpan], v[kSpan];
         const T *xr = reinterpret_cast<const T *>(mine + stage * kRows);
         const G *gr = reinterpret_cast<const G *>(mine + stage * kRows + kRowsX);
 #pragma unroll
         for (int i = 0; i < kSpan; ++i) {
-            float2 w;
-            gate<COMP>(load2(gr + i * kCh, lane), &a[i], &w);
+            const float2 gi = load2(gr + i * kCh, lane);
+            a[i] = decay(gi);
             v[i] = load2(xr + i * kCh, lane);
-            if (COMP) v[i] = mul2(w, v[i]);
+            if (COMP) v[i] = mul2(strength(gi, a[i]), v[i]);
         }
-        __syncwarp();
-        fetch(step + stages, stage);
+        const float4 own = plain ? map_span<true>(p, u, a, v, 0, nullptr, c)
+                                 : map_span<false>(p, u, a, v, m.starts, start_of, c);
+        sh.spans[warp][lane] = own;
+        if (lane == 0) sh.cut[warp] = m.starts != 0;
+        const bool any = __syncthreads_or(m.starts != 0);
+        // the map of the spans before this one
+        float2 PA = both(1.f), PX = both(0.f);
+        bool cut = false;
+        if (!any) {
 #pragma unroll
-        for (int i = 0; i < kSpan; ++i) {
-            if (m.starts >> i & 1) X = load_state(p.h0, start_of[warp][i] * p.D + u.c0 + 2 * lane, u.mine);
-            X = fma2(a[i], X, v[i]);
-            A = mul2(A, a[i]);
-        }
-        spans[buf][warp][lane] = make_float4(A.x, X.x, A.y, X.y);
-        if (lane == 0) span_cut[buf][warp] = m.starts != 0;
-        __syncthreads();
-        // the maps of the spans before this one, and of the tile
-        float2 PA, PX, QA = make_float2(1.f, 1.f), QX = make_float2(0.f, 0.f), h;
-        int pcut, qcut = 0;
-#pragma unroll
-        for (int j = 0; j < kWarps; ++j) {
-            if (j == warp) PA = QA, PX = QX, pcut = qcut;
-            const float4 s = spans[buf][j][lane];
-            if (span_cut[buf][j]) qcut = 1, QX = make_float2(0.f, 0.f);
-            QX = make_float2(fmaf(s.x, QX.x, s.y), fmaf(s.z, QX.y, s.w));
-            QA = make_float2(QA.x * s.x, QA.y * s.z);
-        }
-        // the state that enters the span, and the next step
-        if (cluster == 1) {
-            h = pcut ? PX : fma2(PA, carry, PX);
-            carry = qcut ? QX : fma2(QA, carry, QX);
+            for (int j = 0; j < kWarps - 1; ++j)
+                if (j < warp) {
+                    const float4 s = sh.spans[j][lane];
+                    PX = fma2(make_float2(s.x, s.z), PX, make_float2(s.y, s.w));
+                    PA = mul2(PA, make_float2(s.x, s.z));
+                }
         } else {
-            for (int r = warp; r < cluster; r += kWarps) {
-                cluster_store(cluster_addr(&tiles[buf][u.rank][lane], r), make_float4(QA.x, QX.x, QA.y, QX.y));
-                if (lane == 0) cluster_store(cluster_addr(&tile_cut[buf][u.rank], r), qcut);
-            }
-            cluster_sync();
-            for (int j = 0; j < cluster; ++j) {
-                if (j == u.rank) h = pcut ? PX : fma2(PA, carry, PX);
-                const float4 s = tiles[buf][j][lane];
-                carry = tile_cut[buf][j] ? make_float2(s.y, s.w) : make_float2(fmaf(s.x, carry.x, s.y), fmaf(s.z, carry.y, s.w));
+            for (int j = 0; j < warp; ++j) {
+                const float4 s = sh.spans[j][lane];
+                const bool here = sh.cut[j] & 1;
+                PX = join(s, here, PX);
+                PA = mul2(PA, make_float2(s.x, s.z));
+                cut |= here;
             }
         }
-        // the span's tokens
-        if (p.states && warp == 0 && t0 < t1 && p.tiles > 1)
-            store_state(p.states, (u.tile0 + t0 / kTile) * p.D + u.c0 + 2 * lane, h, u.mine);
-#pragma unroll
-        for (int i = 0; i < kSpan; ++i) {
-            if (m.starts >> i & 1) h = load_state(p.h0, start_of[warp][i] * p.D + u.c0 + 2 * lane, u.mine);
-            h = fma2(a[i], h, v[i]);
-            if (o && t0 + i < t1) store_pair<EVEN>(o + (t0 + i) * p.os, h, u.mine);
-            if (m.ends >> i & 1) store_state(p.hT, end_of[warp][i] * p.D + u.c0 + 2 * lane, h, u.mine);
+        float4 q;
+        bool qcut;
+        if (warp == kWarps - 1) {
+            const float2 X = join(own, m.starts != 0, PX);
+            q = make_float4(PA.x * own.x, X.x, PA.y * own.z, X.y);
+            qcut = cut || m.starts != 0;
+            send_map(p, sh, u.rank, step, lane, q, qcut);
         }
+        fetch(step + stages, stage);
+        next = marks(step + 1);
+        if (warp == kWarps - 1) carry_on<false>(p, sh, u.rank, step, lane, q, qcut, &carry);
+        __syncthreads();
+        if (sh.dead) break;
+        const float2 h = cut ? PX : fma2(PA, sh.enter[lane], PX);
+        if (p.states && at % kSaved == 0 && count)
+            store_state(p.states, (u.saved0 + at / kSaved) * p.D + c, h, u.mine);
+        if (plain)
+            run_span<true, EVEN>(p, u, a, v, h, m, count, start_of, end_of, c, o ? o + at * p.os : nullptr);
+        else
+            run_span<false, EVEN>(p, u, a, v, h, m, count, start_of, end_of, c, o ? o + at * p.os : nullptr);
     }
+    copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
+    cluster_end(cluster);
 }
 
 // ---------------------------------------------------------------- backward
-template <typename T, typename G, bool COMP, bool EVEN>
-__global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float4 spans[2][kWarps][32], tiles[2][kMaxCluster][32];  // (A, X), (A, Y) of two channels
-    __shared__ float2 grads[2][kWarps][32];                             // Y
-    __shared__ int span_cut[2][kWarps], tile_cut[2][kMaxCluster];       // bit 0: forward, bit 1: backward
-    __shared__ int start_of[kWarps][kSpan], end_of[kWarps][kSpan];
-    constexpr int kRowsX = kSpan * kCh * sizeof(T), kRows = 2 * kRowsX + kSpan * kCh * sizeof(G);
+// A token's two channels as they are kept in registers.
+__device__ __forceinline__ float2 raw(const float *p, int lane) { return load2(p, lane); }
+__device__ __forceinline__ __nv_bfloat162 raw(const __nv_bfloat16 *p, int lane) {
+    return reinterpret_cast<const __nv_bfloat162 *>(p)[lane];
+}
+__device__ __forceinline__ float2 value(float2 v) { return v; }
+__device__ __forceinline__ float2 value(__nv_bfloat162 v) { return __bfloat1622float2(v); }
 
+// The reverse map of a span.
+template <bool PLAIN, int kSpan, typename R>
+__device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                           const R (&d)[kSpan], uint32_t ends, const int *end_of, int64_t c) {
+    float2 Y = both(0.f);
+#pragma unroll
+    for (int i = kSpan - 1; i >= 0; --i) {
+        if (!PLAIN && (ends >> i & 1)) Y = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
+        Y = mul2(a[i], add2(value(d[i]), Y));
+    }
+    return Y;
+}
+
+// The span's tokens: the states before them, then the gradients from the last to the first.
+template <bool PLAIN, bool COMP, bool EVEN, int kSpan, typename R, typename T, typename G>
+__device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                         const float2 (&w)[kSpan], const R (&x)[kSpan], const R (&d)[kSpan], float2 h,
+                                         float2 r, Marks m, int count, const int *start_of, const int *end_of,
+                                         int64_t c, T *dx, G *dg) {
+    float2 before[kSpan];
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+        if (!PLAIN && (m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        const float2 v = value(x[i]);
+        before[i] = COMP ? make_float2(h.x - v.x, h.y - v.y) : h;
+        h = fma2(a[i], h, COMP ? mul2(w[i], v) : v);
+    }
+#pragma unroll
+    for (int i = kSpan - 1; i >= 0; --i) {
+        if (!PLAIN && (m.ends >> i & 1)) r = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
+        const float2 e = add2(value(d[i]), r);
+        r = mul2(a[i], e);
+        if (PLAIN || i < count) {
+            store_pair<EVEN>(dx + i * p.dxs, COMP ? mul2(w[i], e) : e, u.mine);
+            store_pair<EVEN>(dg + i * p.dgs, mul2(r, before[i]), u.mine);
+        }
+        if (!PLAIN && (m.starts >> i & 1)) store_state(p.dh0, start_of[i] * p.D + c, r, u.mine);
+    }
+}
+
+template <int kSpan, typename T, typename G, bool COMP, bool EVEN>
+__global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Shared sh;
+    constexpr int kTile = kSpan * kWarps;
+    static_assert(kTile == kSaved, "a tile starts from a saved state");
+    constexpr int kRowsX = kSpan * kCh * sizeof(T), kRows = 2 * kRowsX + kSpan * kCh * sizeof(G);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, stages = p.stages;
-    const Unit u = unit_of(p, lane);
+    const Unit u = unit_of(p, kTile, lane);
+    const int64_t c = u.c0 + 2 * lane;
+    cluster_begin(sh, cluster);
+
     unsigned char *mine = smem + (size_t)warp * stages * kRows;
     const T *x = static_cast<const T *>(p.x) + u.tok0 * p.xs + u.c0;
     const T *dy = static_cast<const T *>(p.dy) + u.tok0 * p.os + u.c0;
     const G *g = static_cast<const G *>(p.g) + u.tok0 * p.gs + u.c0;
-    T *dx = static_cast<T *>(p.dx) + u.tok0 * p.dxs + u.c0 + 2 * lane;
-    G *dg = static_cast<G *>(p.dg) + u.tok0 * p.dgs + u.c0 + 2 * lane;
+    T *dx = static_cast<T *>(p.dx) + u.tok0 * p.dxs + c;
+    G *dg = static_cast<G *>(p.dg) + u.tok0 * p.dgs + c;
     // steps count from the stream's end
     const auto first_token = [&](int step) {
         return ((int64_t)(u.steps - 1 - step) * cluster + u.rank) * kTile + warp * kSpan;
@@ -435,110 +656,106 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(const __grid
             const int64_t t0 = first_token(step);
             const int rows = t0 >= u.S ? 0 : u.S - t0 < kSpan ? (int)(u.S - t0) : kSpan;
             unsigned char *to = mine + stage * kRows;
-            copy_rows(reinterpret_cast<T *>(to), rows ? x + t0 * p.xs : x, p.xs, rows, u.cols, p.wide, p.even, lane);
-            copy_rows(reinterpret_cast<T *>(to + kRowsX), rows ? dy + t0 * p.os : dy, p.os, rows, u.cols, p.wide, p.even, lane);
-            copy_rows(reinterpret_cast<G *>(to + 2 * kRowsX), rows ? g + t0 * p.gs : g, p.gs, rows, u.cols, p.wide, p.even, lane);
+            copy_rows<kSpan>(reinterpret_cast<T *>(to), rows ? x + t0 * p.xs : x, p.xs, rows, u.cols, p.wide, p.even, lane);
+            copy_rows<kSpan>(reinterpret_cast<T *>(to + kRowsX), rows ? dy + t0 * p.os : dy, p.os, rows, u.cols, p.wide, p.even, lane);
+            copy_rows<kSpan>(reinterpret_cast<G *>(to + 2 * kRowsX), rows ? g + t0 * p.gs : g, p.gs, rows, u.cols, p.wide, p.even, lane);
         }
         copy_commit();
     };
-    for (int i = 0; i < stages; ++i) fetch(i, i);
-    if (cluster > 1) cluster_sync();
-
     Seq seq = {0, 0, 0};
-    float2 carry = make_float2(0.f, 0.f);  // gradient of the state that leaves the cluster's step
-    for (int step = 0, stage = 0; step < u.steps; ++step, stage = stage + 1 == stages ? 0 : stage + 1) {
-        const int buf = step & 1;
+    const auto marks = [&](int step) {
+        if (step >= u.steps) return Marks{0, 0};
         const int64_t at = first_token(step);
         const int t0 = at < u.S ? (int)at : u.S, t1 = u.S - t0 < kSpan ? u.S : t0 + kSpan;
-        // the state that enters the tile (the first tile starts a sequence)
-        const int64_t tile = (at - warp * kSpan) / kTile;
-        float2 h = make_float2(0.f, 0.f);
-        if (tile > 0 && tile < p.tiles) h = load_state(p.states, (u.tile0 + tile) * p.D + u.c0 + 2 * lane, u.mine);
-        __syncwarp();
-        const Marks m = mark(p, u.first, u.S, t0, t1, lane, &seq, start_of[warp], end_of[warp]);
+        return mark(p, u.first, u.S, t0, t1, lane, &seq, sh.start_of[step & 1][warp], sh.end_of[step & 1][warp]);
+    };
+    // the state that enters a step's tile (the stream's first tile starts a sequence)
+    const auto saved = [&](int step) {
+        const int64_t tile = step < u.steps ? (first_token(step) - warp * kSpan) / kTile : 0;
+        return tile > 0 && tile < p.saved ? load_state(p.states, (u.saved0 + tile) * p.D + c, u.mine) : both(0.f);
+    };
+    for (int i = 0; i < stages; ++i) fetch(i, i);
+    Marks next = marks(0);
+    float2 enter = saved(0);
+    float2 carry = both(0.f);  // the gradient of the state that leaves the step (the first warp's)
+    cluster_ready(cluster);
+
+    for (int step = 0, stage = 0; step < u.steps; ++step, stage = stage + 1 == stages ? 0 : stage + 1) {
+        const Marks m = next;
+        const int *start_of = sh.start_of[step & 1][warp], *end_of = sh.end_of[step & 1][warp];
+        const int64_t at = first_token(step);
+        const int count = at >= u.S ? 0 : u.S - at < kSpan ? (int)(u.S - at) : kSpan;
+        const bool plain = !(m.starts | m.ends) && count == kSpan;
         copy_wait(stages - 1);
         __syncwarp();
+        float2 a[kSpan], w[kSpan];
+        decltype(raw((const T *)nullptr, 0)) xv[kSpan], dv[kSpan];
         const T *xr = reinterpret_cast<const T *>(mine + stage * kRows);
         const T *dr = reinterpret_cast<const T *>(mine + stage * kRows + kRowsX);
         const G *gr = reinterpret_cast<const G *>(mine + stage * kRows + 2 * kRowsX);
-        // the span's maps
-        float2 a[kSpan], w[kSpan], A = make_float2(1.f, 1.f), X = make_float2(0.f, 0.f), Y = X;
+        float2 v[kSpan];
 #pragma unroll
         for (int i = 0; i < kSpan; ++i) {
-            gate<COMP>(load2(gr + i * kCh, lane), &a[i], &w[i]);
-            if (m.starts >> i & 1) X = load_state(p.h0, start_of[warp][i] * p.D + u.c0 + 2 * lane, u.mine);
-            const float2 v = load2(xr + i * kCh, lane);
-            X = fma2(a[i], X, COMP ? mul2(w[i], v) : v);
-            A = mul2(A, a[i]);
+            const float2 gi = load2(gr + i * kCh, lane);
+            a[i] = decay(gi);
+            w[i] = COMP ? strength(gi, a[i]) : both(1.f);
+            xv[i] = raw(xr + i * kCh, lane);
+            dv[i] = raw(dr + i * kCh, lane);
+            v[i] = COMP ? mul2(w[i], value(xv[i])) : value(xv[i]);
         }
-#pragma unroll
-        for (int i = kSpan - 1; i >= 0; --i) {
-            if (m.ends >> i & 1) Y = load_state(p.dhT, end_of[warp][i] * p.D + u.c0 + 2 * lane, u.mine);
-            const float2 d = load2(dr + i * kCh, lane);
-            Y = mul2(a[i], make_float2(d.x + Y.x, d.y + Y.y));
-        }
-        spans[buf][warp][lane] = make_float4(A.x, X.x, A.y, X.y);
-        grads[buf][warp][lane] = Y;
-        if (lane == 0) span_cut[buf][warp] = (m.starts != 0) | (m.ends != 0) << 1;
+        const float4 f = plain ? map_span<true>(p, u, a, v, 0, nullptr, c)
+                               : map_span<false>(p, u, a, v, m.starts, start_of, c);
+        const float2 Y = plain ? map_back<true>(p, u, a, dv, 0, nullptr, c)
+                               : map_back<false>(p, u, a, dv, m.ends, end_of, c);
+        const float4 own = make_float4(f.x, Y.x, f.z, Y.y);
+        sh.spans[warp][lane] = own;
+        sh.starts[warp][lane] = make_float2(f.y, f.w);
+        if (lane == 0) sh.cut[warp] = (m.starts != 0) | (m.ends != 0) << 1;
         __syncthreads();
-        // the state that enters the span
-        for (int j = 0; j < warp; ++j) {
-            const float4 s = spans[buf][j][lane];
-            if (span_cut[buf][j] & 1) h = make_float2(0.f, 0.f);
-            h = make_float2(fmaf(s.x, h.x, s.y), fmaf(s.z, h.y, s.w));
-        }
-        // the reverse maps of the spans after this one, and of the tile
-        float2 PA, PY, QA = make_float2(1.f, 1.f), QY = make_float2(0.f, 0.f), r;
-        int pcut, qcut = 0;
+        // the reverse map of the spans after this one
+        float2 PA = both(1.f), PY = both(0.f);
+        bool cut = false;
 #pragma unroll
-        for (int j = kWarps - 1; j >= 0; --j) {
-            if (j == warp) PA = QA, PY = QY, pcut = qcut;
-            const float4 s = spans[buf][j][lane];
-            const float2 y = grads[buf][j][lane];
-            if (span_cut[buf][j] & 2) qcut = 1, QY = make_float2(0.f, 0.f);
-            QY = make_float2(fmaf(s.x, QY.x, y.x), fmaf(s.z, QY.y, y.y));
-            QA = make_float2(QA.x * s.x, QA.y * s.z);
-        }
-        // the gradient of the state that leaves the span, and the next step
-        if (cluster == 1) {
-            r = pcut ? PY : fma2(PA, carry, PY);
-            carry = qcut ? QY : fma2(QA, carry, QY);
-        } else {
-            for (int k = warp; k < cluster; k += kWarps) {
-                cluster_store(cluster_addr(&tiles[buf][u.rank][lane], k), make_float4(QA.x, QY.x, QA.y, QY.y));
-                if (lane == 0) cluster_store(cluster_addr(&tile_cut[buf][u.rank], k), qcut);
+        for (int j = kWarps - 1; j > 0; --j)
+            if (j > warp) {
+                const float4 s = sh.spans[j][lane];
+                const bool here = sh.cut[j] & 2;
+                PY = join(s, here, PY);
+                PA = mul2(PA, make_float2(s.x, s.z));
+                cut |= here;
             }
-            cluster_sync();
-            for (int j = cluster - 1; j >= 0; --j) {
-                if (j == u.rank) r = pcut ? PY : fma2(PA, carry, PY);
-                const float4 s = tiles[buf][j][lane];
-                carry = tile_cut[buf][j] ? make_float2(s.y, s.w) : make_float2(fmaf(s.x, carry.x, s.y), fmaf(s.z, carry.y, s.w));
-            }
+        float4 q;
+        bool qcut;
+        if (warp == 0) {
+            const float2 R = join(own, m.ends != 0, PY);
+            q = make_float4(PA.x * own.x, R.x, PA.y * own.z, R.y);
+            qcut = cut || m.ends != 0;
+            send_map(p, sh, u.rank, step, lane, q, qcut);
         }
-        // the span's tokens: the states before them, then the gradients from the last to the first
-        float2 before[kSpan];
-#pragma unroll
-        for (int i = 0; i < kSpan; ++i) {
-            if (m.starts >> i & 1) h = load_state(p.h0, start_of[warp][i] * p.D + u.c0 + 2 * lane, u.mine);
-            const float2 v = load2(xr + i * kCh, lane);
-            before[i] = COMP ? make_float2(h.x - v.x, h.y - v.y) : h;
-            h = fma2(a[i], h, COMP ? mul2(w[i], v) : v);
-        }
-#pragma unroll
-        for (int i = kSpan - 1; i >= 0; --i) {
-            if (m.ends >> i & 1) r = load_state(p.dhT, end_of[warp][i] * p.D + u.c0 + 2 * lane, u.mine);
-            const float2 d = load2(dr + i * kCh, lane), e = make_float2(d.x + r.x, d.y + r.y);
-            r = mul2(a[i], e);
-            if (t0 + i < t1) {
-                store_pair<EVEN>(dx + (t0 + i) * p.dxs, COMP ? mul2(w[i], e) : e, u.mine);
-                store_pair<EVEN>(dg + (t0 + i) * p.dgs, mul2(r, before[i]), u.mine);
-            }
-            if (m.starts >> i & 1) store_state(p.dh0, start_of[warp][i] * p.D + u.c0 + 2 * lane, r, u.mine);
-        }
-        __syncwarp();
         fetch(step + stages, stage);
+        next = marks(step + 1);
+        // the state that enters the span
+        float2 h = enter;
+        enter = saved(step + 1);
+#pragma unroll
+        for (int j = 0; j < kWarps - 1; ++j)
+            if (j < warp) {
+                const float4 s = sh.spans[j][lane];
+                const float2 X = sh.starts[j][lane];
+                h = sh.cut[j] & 1 ? X : fma2(make_float2(s.x, s.z), h, X);
+            }
+        if (warp == 0) carry_on<true>(p, sh, u.rank, step, lane, q, qcut, &carry);
+        __syncthreads();
+        if (sh.dead) break;
+        const float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
+        if (plain)
+            run_back<true, COMP, EVEN>(p, u, a, w, xv, dv, h, r, m, count, start_of, end_of, c, dx + at * p.dxs, dg + at * p.dgs);
+        else
+            run_back<false, COMP, EVEN>(p, u, a, w, xv, dv, h, r, m, count, start_of, end_of, c, dx + at * p.dxs, dg + at * p.dgs);
     }
+    copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
+    cluster_end(cluster);
 }
 
 // ---------------------------------------------------------------- one-token form
@@ -555,7 +772,8 @@ __global__ void __launch_bounds__(128) linrec_decode_kernel(LinrecParams p, floa
     float h = state[n * p.D + c];
     for (int64_t t = n * p.T; t < (n + 1) * p.T; ++t) {
         const float gt = ld(g, t * p.gs + c), xt = ld(x, t * p.xs + c);
-        h = fmaf(__expf(gt), h, COMP ? -expm1f(gt) * xt : xt);
+        const float2 a = decay(make_float2(gt, 0.f));
+        h = fmaf(a.x, h, COMP ? strength(make_float2(gt, 0.f), a).x * xt : xt);
         put(o + t * p.os + c, h);
     }
     state[n * p.D + c] = h;
@@ -580,7 +798,7 @@ cudaError_t launch_cluster(void (*kernel)(LinrecParams), std::atomic<uint64_t> *
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.streams * p.slabs * p.cluster));
-    cfg.blockDim = dim3(32 * kWarps);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -592,28 +810,39 @@ cudaError_t launch_cluster(void (*kernel)(LinrecParams), std::atomic<uint64_t> *
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Tokens per warp: 16 in the forward of bf16 inputs, whose factors and inputs then take 64
+// registers and whose tiles 32 or 48 KB; 8 where a tile of 16 would not leave room for two CTAs
+// and a second stage.
+template <typename T> constexpr int kFwdSpan = sizeof(T) == 2 ? 16 : 8;
+constexpr int kBwdSpan = 8;
+
 template <typename T, typename G, bool COMP, bool EVEN>
 cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
     static std::atomic<uint64_t> ready[2];
-    const size_t rows = (size_t)kTile * kCh * (pass == Pass::kFwd ? sizeof(T) + sizeof(G) : 2 * sizeof(T) + sizeof(G));
+    const bool fwd = pass == Pass::kFwd;
+    const int64_t tile = kWarps * (fwd ? kFwdSpan<T> : kBwdSpan);
+    const size_t bytes = tile * kCh * (fwd ? sizeof(T) + sizeof(G) : 2 * sizeof(T) + sizeof(G));
+    const int64_t tiles = (p.rows_per_stream * p.T + tile - 1) / tile;
     // CTAs: as many as give every SM kPerSm of them, in clusters no longer than the stream
     const int64_t units = p.streams * p.slabs;
     p.cluster = 1;
-    while (p.cluster < kMaxCluster && 2 * p.cluster <= p.tiles && units * p.cluster * 2 <= kSms * kPerSm) p.cluster *= 2;
+    while (p.cluster < kMaxCluster && 2 * p.cluster <= tiles && units * p.cluster * 2 <= kSms * kPerSm) p.cluster *= 2;
     // stages: what the SM's shared memory holds for the CTAs that it gets, up to the steps there are
     const int64_t per_sm = (units * p.cluster + kSms - 1) / kSms;
-    const int64_t steps = (p.tiles + p.cluster - 1) / p.cluster;
-    const size_t room = kSmemSm / (per_sm < 1 ? 1 : per_sm > kPerSm ? kPerSm : per_sm) - kSmemStatic;
-    int64_t stages = (int64_t)((room < kSmemMax ? room : kSmemMax) / rows);
+    const int64_t steps = (tiles + p.cluster - 1) / p.cluster;
+    const size_t room = kSmemSm / (per_sm < 1 ? 1 : per_sm > kPerSm ? kPerSm : per_sm) - kSmemStatic - 1024;
+    int64_t stages = (int64_t)((room < kSmemMax ? room : kSmemMax) / bytes);
     if (stages > kMaxStages) stages = kMaxStages;
     if (stages > steps) stages = steps;
     p.stages = stages < 1 ? 1 : (int32_t)stages;
-    const size_t smem = rows * p.stages;
+    const size_t smem = bytes * p.stages;
+    p.wait_limit = call_wait_limit();
+    p.test_hook = call_test_hook();
     cudaError_t err = cudaSuccess;
-    if (pass == Pass::kFwd)
-        GDN_LAUNCH(kKLinrecFwd, s, (err = launch_cluster(linrec_fwd_kernel<T, G, COMP, EVEN>, &ready[0], p, smem, s)));
+    if (fwd)
+        GDN_LAUNCH(kKLinrecFwd, s, (err = launch_cluster(linrec_fwd_kernel<kFwdSpan<T>, T, G, COMP, EVEN>, &ready[0], p, smem, s)));
     else
-        GDN_LAUNCH(kKLinrecBwd, s, (err = launch_cluster(linrec_bwd_kernel<T, G, COMP, EVEN>, &ready[1], p, smem, s)));
+        GDN_LAUNCH(kKLinrecBwd, s, (err = launch_cluster(linrec_bwd_kernel<kBwdSpan, T, G, COMP, EVEN>, &ready[1], p, smem, s)));
     return err;
 }
 
@@ -671,9 +900,9 @@ gdn_status describe(const gdn_linrec_desc *d, LinrecParams *p) {
     p->D = d->D;
     p->N = d->n_seqs > 0 ? d->n_seqs : d->B;
     // streams: the packed row, a dense row, or as many short dense rows as fill a tile
-    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kTile ? kTile / p->T : 1;
+    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kSaved ? kSaved / p->T : 1;
     p->streams = d->n_seqs > 0 ? 1 : (p->N + p->rows_per_stream - 1) / p->rows_per_stream;
-    p->tiles = (p->rows_per_stream * p->T + kTile - 1) / kTile;
+    p->saved = (p->rows_per_stream * p->T + kSaved - 1) / kSaved;
     p->slabs = (int32_t)((p->D + kCh - 1) / kCh);
     if (p->streams * p->slabs >= kLim / kMaxCluster) return GDN_ERR_INVALID_ARG;
     const int64_t in[] = {d->x_stride, d->g_stride, d->o_stride, d->dx_stride, d->dg_stride};
@@ -689,7 +918,7 @@ bool mis(const void *p, size_t a = 16) { return p && (reinterpret_cast<uintptr_t
 
 // A stream of one tile needs none: every sequence starts within it.
 size_t states_bytes(const LinrecParams &p) {
-    const size_t b = p.tiles > 1 ? (size_t)p.streams * p.tiles * p.D * sizeof(float) : 0;
+    const size_t b = p.saved > 1 ? (size_t)p.streams * p.saved * p.D * sizeof(float) : 0;
     return b < 256 ? 256 : (b + 255) / 256 * 256;
 }
 
@@ -722,6 +951,16 @@ gdn_status check_seqlens(const gdn_linrec_desc *d, const int32_t *cu_dev, const 
 
 extern "C" {
 
+gdn_status gdn_linrec_status(void *stream) {
+    using namespace gdn;
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GDN_ERR_CUDA;
+    int32_t status = 0;
+    if (cudaMemcpyFromSymbol(&status, g_status, sizeof(status)) != cudaSuccess) return GDN_ERR_CUDA;
+    const int32_t zero = 0;
+    if (status != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return GDN_ERR_CUDA;
+    return static_cast<gdn_status>(status);
+}
+
 size_t gdn_linrec_states_size(const gdn_linrec_desc *desc) {
     gdn::LinrecParams p{};
     return gdn::describe(desc, &p) == GDN_OK ? gdn::states_bytes(p) : 0;
@@ -742,7 +981,7 @@ gdn_status gdn_linrec_fwd(const gdn_linrec_desc *desc, const void *x, const void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = check_seqlens(desc, cu_seqlens, cu_seqlens_host, s)) != GDN_OK) return st;
     p.cu = desc->n_seqs > 0 ? cu_seqlens : nullptr;
-    p.x = x, p.g = g, p.h0 = h0, p.o = o, p.hT = hT, p.states = states;
+    p.x = x, p.g = g, p.h0 = h0, p.o = o, p.hT = hT, p.states = p.saved > 1 ? states : nullptr;
     arm_planted_failure();
     const cudaError_t e = p.BT == 0 ? pass_all(p, h0, hT, s) : launch(desc, p, Pass::kFwd, nullptr, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -774,7 +1013,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void
     p.states = const_cast<float *>(states);
     arm_planted_failure();
     if (p.BT == 0) return pass_all(p, dhT, dh0, s) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-    if (!states && p.tiles > 1) {
+    if (!states && p.saved > 1) {
         p.states = static_cast<float *>(workspace);
         if (launch(desc, p, Pass::kFwd, nullptr, s) != cudaSuccess) return GDN_ERR_CUDA;
     }

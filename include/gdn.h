@@ -270,6 +270,12 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void
                           float *dh0, const float *states, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/* Synchronises the stream, then returns and clears the device-side status of
+ * the gdn_linrec_fwd and gdn_linrec_bwd calls on the current device: GDN_OK, or
+ * GDN_ERR_TIMEOUT when a bounded wait between the CTAs of a cluster ran out (the
+ * call's outputs are then undefined).  GDN_ERR_CUDA if the stream failed. */
+gdn_status gdn_linrec_status(void *stream);
+
 /* One-token form for inference: advances state [B][D] (fp32, in place) through
  * the T tokens (usually 1) of each of the B rows; n_seqs must be 0, T >= 1. */
 gdn_status gdn_linrec_decode(const gdn_linrec_desc *desc, const void *x, const void *g,
@@ -351,8 +357,8 @@ const char *gdn_status_string(gdn_status status);
  * without faulting a GPU).  Both apply to every later call from the calling
  * thread until changed; the defaults are 0.
  *
- * gdn_set_wait_limit: every bounded device-side wait of the tensor-core
- * kernels gives up after `polls` polls of its mbarrier instead of the built-in
+ * gdn_set_wait_limit: every bounded device-side wait (of the tensor-core kernels
+ * and of gdn_linrec_*) gives up after `polls` polls of its mbarrier instead of the built-in
  * 2^23 (about a second); 0 restores the built-in limit.  A wait that gives up
  * records GDN_ERR_TIMEOUT, and the kernels of the call that start after it
  * return at once (read it with gdn_device_status).
@@ -362,7 +368,9 @@ const char *gdn_status_string(gdn_status status);
  *                        preparation step arms its input-copy mbarrier for 16
  *                        bytes more than its copies bring: every copy lands,
  *                        the wait runs out, and the call records
- *                        GDN_ERR_TIMEOUT (outputs are then undefined).
+ *                        GDN_ERR_TIMEOUT (outputs are then undefined).  In
+ *                        gdn_linrec_fwd and gdn_linrec_bwd the first CTA of a
+ *                        cluster waits for 16 bytes more than the others send.
  *   GDN_TEST_FAIL_LAUNCH the call's first kernel launch is skipped and treated
  *                        as a failed launch: the call returns GDN_ERR_CUDA.
  * 0 removes the hook. */

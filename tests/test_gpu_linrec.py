@@ -305,6 +305,25 @@ def test_planted_launch_failure_is_reported():
     run_and_check(v)
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """The first CTA waits for 16 bytes more than its cluster sends: it gives up after the limit,
+    then so do the others, and the kernel ends."""
+    v = draw(1, 2000, 64, seed=4)
+    d = {k: t.cuda() for k, t in v.items()}
+    gdn.set_wait_limit(1 << 12)
+    gdn.set_test_hook(gdn.GDN_TEST_STALL_COPY)
+    try:
+        _, _, states = gdn.gdn_linrec_fwd(d["x"], d["g"], save_states=True)
+        assert gdn.linrec_status() == 6 and gdn.linrec_status() == 0
+        gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], states=states)
+        assert gdn.linrec_status() == 6
+    finally:
+        gdn.set_test_hook(0)
+        gdn.set_wait_limit(0)
+    run_and_check(v)
+    assert gdn.linrec_status() == 0
+
+
 def test_launch_trace_names_the_kernels():
     v = draw(1, 300, 64)
     d = {k: t.cuda() for k, t in v.items()}
