@@ -4,25 +4,24 @@
 // A sequence's map over any span of tokens is affine per channel, h' = A h + X with
 // A the product of the span's factors, and the reverse map of the gradients is
 // r' = A r + Y with the same A; spans join by (A2, X2)(A1, X1) = (A2 A1, A2 X1 + X2).
-// A CTA takes 64 channels (two per lane) and a tile of tokens at a time, split into one
-// span per warp, whose tokens stay in registers.  Each of eight warps forms its span's A
-// and X (and Y) and joins the spans before it; the last one, which thereby has the tile's
-// map, carries the state.  A cluster of up to 16 CTAs takes consecutive tiles of the same
-// channels: the carrying warps send their tile's map to all of them (st.async into
-// distributed shared memory, counted by an mbarrier: no cluster barrier, whose release
+// A CTA takes 64 channels (two per lane) and a tile of 64 M tokens at a time, 8 M adjacent
+// tokens per warp, which stay in shared memory through two passes: the first forms the
+// warp's map, the second runs its tokens from the state that enters them and refills each
+// 8 tokens' place with the next tile's, so copies are on their way during the second pass.
+// In between, the warps join the maps before theirs; the last one, which thereby has the
+// tile's map, carries the state.  A cluster of up to 16 CTAs takes consecutive tiles of the
+// same channels: the carrying warps send their tile's map to all of them (one bulk copy each
+// through distributed shared memory, counted by an mbarrier: a cluster barrier's release
 // would wait for the outputs still being stored) and each folds them in order, so each holds
-// the state that enters its tile and the next step.  Joins go in token order and tile by
-// tile, so results depend neither on the cluster's size nor on timing.  The data is read
-// once: the next steps' tiles are on their way by cp.async, each warp copying the rows
-// that it will use.
+// the state that enters its tile and the next step.  The data is read from memory once.
 //
 // A start of a sequence inside a span drops what comes before it by selection (not by a
 // factor of 0), so that no infinity or NaN crosses; padded tokens are zeros (factor
 // exp(0) = 1, input 0), which is the identity map in both directions.
 //
 // The backward runs the tiles from the last to the first.  It needs the states that
-// enter each token: the forward leaves the state entering every 64th token (4 / 64 bytes
-// per element), from which a tile recomputes its own.
+// enter each token: the forward leaves the state entering every tile of the backward (at
+// most 4 / 64 bytes per element), from which a tile recomputes its own.
 #include <atomic>
 #include <vector>
 
@@ -34,22 +33,24 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCh = 64;                // channels per CTA
-constexpr int kSaved = 64;             // tokens between two saved states
-constexpr int kMaxSpan = 16;
-constexpr int kMaxStages = 8;
+constexpr int kSpan = 8;       // adjacent tokens that a warp has in registers at a time
+constexpr int kRows = kSpan * kWarps;
+constexpr int kCh = 64;        // channels per CTA
+constexpr int kMaxSpans = 8;   // M: spans per warp and tile
 constexpr int kMaxCluster = 16;
-constexpr int kSms = 148, kPerSm = 2;
-constexpr size_t kSmemSm = 227 * 1024, kSmemMax = 200 * 1024, kSmemStatic = 25 * 1024;  // dynamic, static and reserved
+constexpr int kSms = 148, kFwdPerSm = 3, kBwdPerSm = 2;  // CTAs per SM that the registers allow
+constexpr size_t kSmemSm = 227 * 1024, kSmemCta = 9 * 1024 + 256;  // of an SM, and of a CTA beside tiles and maps
 
 struct LinrecParams {
     int64_t T, BT, D, N;
     int64_t xs, gs, os, dxs, dgs;
     int64_t streams, rows_per_stream;  // a stream: one dense row, several short ones, or the packed row
     int64_t saved;                            // saved states of a stream
-    int32_t slabs, cluster, stages, wide, even;
+    int32_t saved_every;                      // tokens between two of them
+    int32_t slabs, cluster, spans, aligned, even;
     uint32_t wait_limit;
     int32_t test_hook;
+    int32_t single;  // every stream is one sequence
     const int32_t *cu;
     const void *x, *g, *dy;
     const float *h0, *dhT;
@@ -139,12 +140,11 @@ __device__ __forceinline__ float2 strength(float2 g, float2 a) {
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
-template <int N>  // copies `bytes` (0 .. N) of N, the rest zeros
-__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {
-    if (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {  // 4, or 4 zeros
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async16(void *dst, const void *src, int bytes) {  // and 16 - bytes zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most `pending` of this thread's groups are unfinished.
@@ -161,20 +161,27 @@ __device__ __forceinline__ void copy_wait(int pending) {
     }
 }
 
-// A warp's copy of its span's tokens x 64 channels; `rows` and `cols` of them exist, the rest become
-// zeros.  wide: 16-byte pieces (rows 16-byte aligned; the last piece may be partial), else 4
-// bytes (fp32, or bf16 with even rows), else one bf16 after another.
-template <int kSpan, typename E>
+// A span's tokens x 64 channels; `rows` and `cols` of them exist, the rest become zeros.  Rows that
+// start on 16 bytes: 16 at a time (the last ones maybe in part); fp32, or bf16 with even rows: 4 at
+// a time; else one bf16 after another.
+template <bool ALIGNED, typename E>
 __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, int rows, int cols,
-                                          int wide, int even, int lane) {
-    if (wide) {
-        constexpr int kPer = 16 / sizeof(E), kPieces = kCh / kPer, kRows = 32 / kPieces;
-        const int c = lane % kPieces * kPer;
+                                          int even, int lane) {
+    if (ALIGNED) {
+        constexpr int kPer = 16 / sizeof(E), kPieces = kCh / kPer, kAtOnce = 32 / kPieces;
+        const int c = lane % kPieces * kPer, r = lane / kPieces;
         const int here = (cols - c) * (int)sizeof(E), bytes = here < 0 ? 0 : here > 16 ? 16 : here;
+        dst += r * kCh + c;
+        if (rows == kSpan) {
+            src += bytes ? r * stride + c : 0;
 #pragma unroll
-        for (int i = 0; i < kSpan; i += kRows) {
-            const int r = i + lane / kPieces, n = r < rows ? bytes : 0;
-            copy_async<16>(dst + r * kCh + c, n ? src + r * stride + c : src, n);
+            for (int i = 0; i < kSpan; i += kAtOnce) copy_async16(dst + i * kCh, src + i * stride, bytes);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSpan; i += kAtOnce) {
+                const int n = i + r < rows ? bytes : 0;
+                copy_async16(dst + i * kCh, n ? src + (i + r) * stride + c : src, n);
+            }
         }
     } else if (sizeof(E) == 4 || even) {
         constexpr int kPer = 4 / sizeof(E);
@@ -183,7 +190,7 @@ __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, 
 #pragma unroll
             for (int c = lane * kPer; c < kCh; c += 32 * kPer) {
                 const bool in = r < rows && c < cols;
-                copy_async<4>(dst + r * kCh + c, in ? src + r * stride + c : src, in ? 4 : 0);
+                copy_async(dst + r * kCh + c, in ? src + r * stride + c : src, in ? 4 : 0);
             }
     } else {
 #pragma unroll 1
@@ -209,16 +216,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
-// Asynchronous stores into a CTA of the cluster; their bytes count down its mbarrier.
-__device__ __forceinline__ void send(uint32_t addr, float4 v, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
-                 ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar) : "memory");
+// Copies shared memory into a CTA of the cluster; its bytes count down that CTA's mbarrier.
+__device__ __forceinline__ void send(uint32_t to, const void *from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "r"(smem_addr(from)), "r"(bytes), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void send(uint32_t addr, int v, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];"
-                 ::"r"(addr), "r"(v), "r"(bar) : "memory");
-}
-constexpr uint32_t kMapBytes = 32 * 16 + 4;  // a tile's map and its cut flag
 
 // Status of this device's calls (gdn_linrec_status).
 __device__ int32_t g_status;
@@ -226,14 +228,13 @@ __device__ int32_t g_status;
 // ---------------------------------------------------------------- sequences of a stream
 // The sequence that holds a token, for a whole warp: index n, tokens [beg, end) of the stream.
 struct Seq {
-    int64_t n;
-    int beg, end;
+    int n, beg, end;
 };
 
 // Moves s to the sequence that holds token t (0 <= t < S).  Packed: the largest n with cu[n]
 // <= t, searched near s first and then 33 ways at a time.  Only cu[1 .. N - 1] are trusted as
 // far as indices go; the bounds are forced around t whatever they hold.
-__device__ __forceinline__ void seek(const LinrecParams &p, int64_t first, int S, int t, int lane, Seq *s) {
+__device__ __forceinline__ void seek(const LinrecParams &p, int first, int S, int t, int lane, Seq *s) {
     if (t >= s->beg && t < s->end) return;
     if (!p.cu) {
         const int T = (int)p.T, k = t / T;
@@ -243,9 +244,9 @@ __device__ __forceinline__ void seek(const LinrecParams &p, int64_t first, int S
     int lo = 0, hi = (int)p.N;  // cu[lo] <= t < cu[hi]
     int step = 1;
     if (t >= s->end) {
-        lo = (int)s->n;
+        lo = s->n;
     } else {
-        hi = s->n > 0 ? (int)s->n : 1;
+        hi = s->n > 0 ? s->n : 1;
         const int at = hi - 1 - lane;
         const bool after = at > lo && p.cu[at] > t;
         const int cnt = __ffs(~__ballot_sync(0xffffffffu, after)) - 1;  // -1: all 32
@@ -279,59 +280,70 @@ __device__ __forceinline__ void seek(const LinrecParams &p, int64_t first, int S
 struct Marks {
     uint32_t starts, ends;
 };
-__device__ __forceinline__ Marks mark(const LinrecParams &p, int64_t first, int S, int t0, int t1, int lane,
+__device__ __forceinline__ Marks mark(const LinrecParams &p, int first, int S, int t0, int t1, int lane,
                                       Seq *s, int *start_of, int *end_of) {
     Marks m = {0, 0};
     if (t0 >= t1) return m;
+    if (p.single) {
+        m.starts = t0 == 0;
+        m.ends = t1 == S ? 1u << (t1 - 1 - t0) : 0;
+        if (lane == 0) {
+            if (m.starts) start_of[0] = first;
+            if (m.ends) end_of[t1 - 1 - t0] = first;
+        }
+        return m;
+    }
     seek(p, first, S, t0, lane, s);
     Seq q = *s;
     if (q.beg == t0) {
         m.starts = 1;
-        if (lane == 0) start_of[0] = (int)q.n;
+        if (lane == 0) start_of[0] = q.n;
     }
     while (true) {
         const int e = q.end;
         if (e <= t1) {
             m.ends |= 1u << (e - 1 - t0);
-            if (lane == 0) end_of[e - 1 - t0] = (int)q.n;
+            if (lane == 0) end_of[e - 1 - t0] = q.n;
         }
         if (e >= t1) break;
         seek(p, first, S, e, lane, &q);
         m.starts |= 1u << (e - t0);
-        if (lane == 0) start_of[e - t0] = (int)q.n;
+        if (lane == 0) start_of[e - t0] = q.n;
     }
     return m;
 }
 
 // What a CTA works on.
 struct Unit {
-    int64_t first;  // first sequence of the stream (dense)
-    int64_t tok0;   // the stream's first token
-    int64_t saved0; // its first saved state
-    int S, steps;   // its tokens, and the cluster's steps over them
-    int64_t c0;
+    int first;   // first sequence of the stream (dense)
+    int tok0;    // the stream's first token
+    int saved0;  // its first saved state
+    int tile;    // tokens of a CTA and step
+    int S, steps;  // its tokens, and the cluster's steps over them
+    int c0;
     int cols, mine;  // channels of the CTA, and of this lane (0, 1 or 2)
     int rank;
 };
-__device__ __forceinline__ Unit unit_of(const LinrecParams &p, int tile, int lane) {
+__device__ __forceinline__ Unit unit_of(const LinrecParams &p, int lane) {
     Unit u;
     u.rank = blockIdx.x % p.cluster;
-    const int64_t i = blockIdx.x / p.cluster, stream = i / p.slabs;
+    const int i = blockIdx.x / p.cluster, stream = i / p.slabs;
     u.c0 = i % p.slabs * kCh;
     u.cols = p.D - u.c0 < kCh ? (int)(p.D - u.c0) : kCh;
     const int left = u.cols - 2 * lane;
     u.mine = left < 0 ? 0 : left > 2 ? 2 : left;
-    u.first = stream * p.rows_per_stream;
+    u.first = stream * (int)p.rows_per_stream;
     if (p.cu) {
         u.tok0 = 0;
         u.S = (int)p.BT;
     } else {
-        const int64_t rows = p.N - u.first < p.rows_per_stream ? p.N - u.first : p.rows_per_stream;
-        u.tok0 = u.first * p.T;
-        u.S = (int)(rows * p.T);
+        const int left_rows = (int)p.N - u.first, rows = left_rows < p.rows_per_stream ? left_rows : (int)p.rows_per_stream;
+        u.tok0 = u.first * (int)p.T;
+        u.S = rows * (int)p.T;
     }
-    u.saved0 = stream * p.saved;
-    u.steps = (int)((u.S + (int64_t)tile * p.cluster - 1) / ((int64_t)tile * p.cluster));
+    u.saved0 = stream * (int)p.saved;
+    u.tile = kRows * p.spans;
+    u.steps = (int)((u.S + (int64_t)u.tile * p.cluster - 1) / ((int64_t)u.tile * p.cluster));
     return u;
 }
 
@@ -352,24 +364,27 @@ __device__ __forceinline__ void pass_empty(const LinrecParams &p, const Unit &u,
 }
 
 // ---------------------------------------------------------------- the carrying warp
-// Shared memory of a CTA.
+// A tile's map; a step's maps, and those of the step before it, are in each CTA of the cluster.
+struct __align__(16) Map {
+    float4 m[32];
+    int cut, pad[3];
+};
+// Shared memory of a CTA, beside its tiles and the cluster's maps.
 struct Shared {
     float4 spans[kWarps][32];               // a span's map (A, X) of the lane's two channels; backward: (A, Y)
     float2 starts[kWarps][32];              // backward: X
-    float4 maps[2][kMaxCluster][32];        // the cluster's tiles' maps
     float2 enter[32];                       // what enters the CTA's tile
-    uint64_t bar[2];                        // arrivals of maps[0], maps[1]
-    int map_cut[2][kMaxCluster];
+    uint64_t bar[2];                        // arrivals of the cluster's maps (even, odd steps)
     int cut[kWarps];                        // bit 0: a start in the span, bit 1: an end
-    int start_of[2][kWarps][kMaxSpan], end_of[2][kWarps][kMaxSpan];
+    int start_of[kWarps][kSpan], end_of[kWarps][kSpan];
     int dead;                               // a wait ran out
+    Map out[2];                             // the tile's map on its way to the cluster (even, odd steps)
 };
-
 __device__ __forceinline__ float2 join(float4 s, bool cut, float2 h) {
     return cut ? make_float2(s.y, s.w) : fma2(make_float2(s.x, s.z), h, make_float2(s.y, s.w));
 }
 
-// Waits (up to `limit` polls) for the phase of this parity: all maps are here.
+// Waits (up to `limit` polls) for the phase of this parity.
 __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, uint32_t limit) {
     for (uint32_t i = 0; i < limit; ++i) {
         uint32_t ok;
@@ -381,18 +396,20 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, uint32_t
     }
     return false;
 }
+__device__ __forceinline__ void give_up(Shared &sh) {
+    sh.dead = 1;
+    g_status = kDevTimeout;
+}
 
 // Makes the mbarriers ready in every CTA of the cluster before anyone sends.
 __device__ __forceinline__ void cluster_begin(Shared &sh, int cluster) {
     if (threadIdx.x == 0) {
         sh.dead = 0;
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.bar[i], 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        ptx::fence_mbar_init();
     }
-    if (cluster > 1)
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    else
-        __syncthreads();
+    __syncthreads();
+    if (cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_ready(int cluster) {
     if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -408,21 +425,22 @@ __device__ __forceinline__ void cluster_end(int cluster) {
 // The carrying warp's part of a step, between the CTA's two barriers: sends the tile's map q to
 // the cluster, forms what enters the tile from all tiles of the step, and the new carry.  REV:
 // from the last rank to the first.
-__device__ __forceinline__ void send_map(const LinrecParams &p, Shared &sh, int rank, int step, int lane, float4 q, bool cut) {
+__device__ __forceinline__ void send_map(const LinrecParams &p, Shared &sh, Map *maps, int rank, int step, int lane, float4 q, bool cut) {
     if (p.cluster == 1) return;
     const int buf = step & 1;
+    Map *to = maps + buf * p.cluster + rank, *out = &sh.out[buf];
+    out->m[lane] = q;
     if (lane == 0) {
+        out->cut = cut;
         const bool stall = p.test_hook == GDN_TEST_STALL_COPY && blockIdx.x == 0 && step == 0;
-        ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * kMapBytes + (stall ? 16 : 0));
+        ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * (uint32_t)sizeof(Map) + (stall ? 16 : 0));
     }
-    for (int r = 0; r < p.cluster; ++r) {
-        const uint32_t bar = cluster_addr(&sh.bar[buf], r);
-        send(cluster_addr(&sh.maps[buf][rank][lane], r), q, bar);
-        if (lane == 0) send(cluster_addr(&sh.map_cut[buf][rank], r), cut, bar);
-    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane < p.cluster) send(cluster_addr(to, lane), out, sizeof(Map), cluster_addr(&sh.bar[buf], lane));
 }
 template <bool REV>
-__device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, int rank, int step, int lane, float4 q, bool cut, float2 *carry) {
+__device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, const Map *maps, int rank, int step, int lane, float4 q, bool cut, float2 *carry) {
     if (p.cluster == 1) {
         sh.enter[lane] = *carry;
         *carry = join(q, cut, *carry);
@@ -430,26 +448,49 @@ __device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, int 
     }
     const int buf = step & 1;
     if (!__all_sync(0xffffffffu, arrived(&sh.bar[buf], (step >> 1) & 1, p.wait_limit))) {
-        if (lane == 0) {
-            sh.dead = 1;
-            g_status = kDevTimeout;
-        }
+        if (lane == 0) give_up(sh);
         return;
     }
+    const Map *from = maps + buf * p.cluster;
     float2 c = *carry;
+#pragma unroll 4
     for (int i = 0; i < p.cluster; ++i) {
         const int j = REV ? p.cluster - 1 - i : i;
         if (j == rank) sh.enter[lane] = c;
-        c = join(sh.maps[buf][j][lane], sh.map_cut[buf][j], c);
+        c = join(from[j].m[lane], from[j].cut, c);
     }
     *carry = c;
 }
 
+// What a warp's spans of a step are, for both passes.
+struct Span {
+    uint32_t t0;  // first token
+    int count;    // tokens (0 .. 8)
+    Marks m;
+    bool plain;   // nothing starts or ends in it, and nothing is missing
+};
+__device__ __forceinline__ Span span_at(const LinrecParams &p, Shared &sh, const Unit &u, uint32_t t0, int warp, int lane, Seq *seq) {
+    Span s;
+    s.t0 = t0;
+    s.count = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
+    __syncwarp();
+    s.m = s.count ? mark(p, u.first, u.S, (int)t0, (int)t0 + s.count, lane, seq, sh.start_of[warp], sh.end_of[warp]) : Marks{0, 0};
+    s.plain = !(s.m.starts | s.m.ends) && s.count == kSpan;
+    __syncwarp();
+    return s;
+}
+
+// Whether the warp's tokens [t0, t0 + n) of a step lie strictly inside one sequence: nothing starts
+// or ends among them, and none is missing.
+__device__ __forceinline__ bool inside(const LinrecParams &p, const Unit &u, const Seq &s, uint32_t t0, uint32_t n) {
+    return p.single ? t0 > 0 && t0 + n < (uint32_t)u.S : (int)t0 > s.beg && t0 + n < (uint32_t)s.end;
+}
+
 // ---------------------------------------------------------------- forward
-// PLAIN: no sequence starts or ends among the span's tokens, and none is missing.
-template <bool PLAIN, int kSpan>
+// A span's map.  PLAIN: no sequence starts in it.
+template <bool PLAIN>
 __device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                           const float2 (&v)[kSpan], uint32_t starts, const int *start_of, int64_t c) {
+                                           const float2 (&v)[kSpan], uint32_t starts, const int *start_of, int c) {
     float2 A = a[0], X = v[0];
     if (!PLAIN && (starts & 1)) X = fma2(a[0], load_state(p.h0, start_of[0] * p.D + c, u.mine), v[0]);
 #pragma unroll
@@ -461,80 +502,95 @@ __device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u,
     return make_float4(A.x, X.x, A.y, X.y);
 }
 
-template <bool PLAIN, bool EVEN, int kSpan, typename T>
-__device__ __forceinline__ void run_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                         const float2 (&v)[kSpan], float2 h, Marks m, int count,
-                                         const int *start_of, const int *end_of, int64_t c, T *o) {
+// The factors and inputs of a span's tokens from shared memory.
+template <bool COMP, typename T, typename G>
+__device__ __forceinline__ void load_span(const T *x, const G *g, int lane, float2 (&a)[kSpan], float2 (&v)[kSpan]) {
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
-        if (!PLAIN && (m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
-        h = fma2(a[i], h, v[i]);
-        if (o && (PLAIN || i < count)) store_pair<EVEN>(o + i * p.os, h, u.mine);
-        if (!PLAIN && (m.ends >> i & 1)) store_state(p.hT, end_of[i] * p.D + c, h, u.mine);
+        const float2 gi = load2(g + i * kCh, lane);
+        a[i] = decay(gi);
+        v[i] = load2(x + i * kCh, lane);
+        if (COMP) v[i] = mul2(strength(gi, a[i]), v[i]);
     }
 }
 
-template <int kSpan, typename T, typename G, bool COMP, bool EVEN>
-__global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
+template <bool PLAIN, bool EVEN, typename T>
+__device__ __forceinline__ float2 run_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                           const float2 (&v)[kSpan], float2 h, const Span &s,
+                                           const int *start_of, const int *end_of, int c, T *o) {
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+        if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        h = fma2(a[i], h, v[i]);
+        if (p.o && (PLAIN || i < s.count)) store_pair<EVEN>(o, h, u.mine);
+        o += p.os;
+        if (!PLAIN && (s.m.ends >> i & 1)) store_state(p.hT, end_of[i] * p.D + c, h, u.mine);
+    }
+    return h;
+}
+
+// ALIGNED: rows start on 16 bytes, and pairs of channels can be stored at once.
+template <typename T, typename G, bool COMP, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
+    extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Shared sh;
-    constexpr int kTile = kSpan * kWarps;
-    constexpr int kRowsX = kSpan * kCh * sizeof(T), kRows = kRowsX + kSpan * kCh * sizeof(G);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, stages = p.stages;
-    const Unit u = unit_of(p, kTile, lane);
-    const int64_t c = u.c0 + 2 * lane;
+    constexpr int kBytesX = kSpan * kCh * sizeof(T), kBytes = kBytesX + kSpan * kCh * sizeof(G);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, M = p.spans;
+    const Unit u = unit_of(p, lane);
+    const int c = u.c0 + 2 * lane;
+    unsigned char *mine = smem + warp * M * kBytes;
+    Map *maps = reinterpret_cast<Map *>(smem + kWarps * M * kBytes);
+    const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
     cluster_begin(sh, cluster);
 
-    unsigned char *mine = smem + (size_t)warp * stages * kRows;
-    const T *x = static_cast<const T *>(p.x) + u.tok0 * p.xs + u.c0;
-    const G *g = static_cast<const G *>(p.g) + u.tok0 * p.gs + u.c0;
-    T *o = p.o ? static_cast<T *>(p.o) + u.tok0 * p.os + c : nullptr;
-    const auto first_token = [&](int step) { return ((int64_t)step * cluster + u.rank) * kTile + warp * kSpan; };
-    const auto fetch = [&](int step, int stage) {
-        const int64_t t0 = first_token(step);
-        if (step < u.steps) {
-            const int rows = t0 >= u.S ? 0 : u.S - t0 < kSpan ? (int)(u.S - t0) : kSpan;
-            unsigned char *to = mine + stage * kRows;
-            copy_rows<kSpan>(reinterpret_cast<T *>(to), rows ? x + t0 * p.xs : x, p.xs, rows, u.cols, p.wide, p.even, lane);
-            copy_rows<kSpan>(reinterpret_cast<G *>(to + kRowsX), rows ? g + t0 * p.gs : g, p.gs, rows, u.cols, p.wide, p.even, lane);
-        }
+    const auto fetch = [&](uint32_t t0, int k) {
+        const int rows = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
+        const int64_t tok = (int64_t)u.tok0 + (rows ? t0 : 0);
+        T *x = reinterpret_cast<T *>(mine + k * kBytes);
+        G *g = reinterpret_cast<G *>(mine + k * kBytes + kBytesX);
+        copy_rows<ALIGNED>(x, static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
+        copy_rows<ALIGNED>(g, static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
         copy_commit();
     };
-    Seq seq = {0, 0, 0};
-    const auto marks = [&](int step) {
-        const int64_t at = first_token(step);
-        const int t0 = at < u.S ? (int)at : u.S, t1 = u.S - t0 < kSpan ? u.S : t0 + kSpan;
-        return step < u.steps ? mark(p, u.first, u.S, t0, t1, lane, &seq, sh.start_of[step & 1][warp], sh.end_of[step & 1][warp]) : Marks{0, 0};
-    };
-    for (int i = 0; i < stages; ++i) fetch(i, i);
-    Marks next = marks(0);
-    float2 carry = both(0.f);  // the state that enters the cluster's step (the last warp's)
+    uint32_t first = u.rank * u.tile + warp * M * kSpan;  // the warp's first token of the step
+    for (int k = 0; k < M; ++k) fetch(first + k * kSpan, k);
     cluster_ready(cluster);
 
-    for (int step = 0, stage = 0; step < u.steps; ++step, stage = stage + 1 == stages ? 0 : stage + 1) {
-        const Marks m = next;
-        const int *start_of = sh.start_of[step & 1][warp], *end_of = sh.end_of[step & 1][warp];
-        const int64_t at = first_token(step);
-        const int count = at >= u.S ? 0 : u.S - at < kSpan ? (int)(u.S - at) : kSpan;
-        const bool plain = !(m.starts | m.ends) && count == kSpan;
-        copy_wait(stages - 1);
-        __syncwarp();
-        float2 a[kSpan], v[kSpan];
-        const T *xr = reinterpret_cast<const T *>(mine + stage * kRows);
-        const G *gr = reinterpret_cast<const G *>(mine + stage * kRows + kRowsX);
-#pragma unroll
-        for (int i = 0; i < kSpan; ++i) {
-            const float2 gi = load2(gr + i * kCh, lane);
-            a[i] = decay(gi);
-            v[i] = load2(xr + i * kCh, lane);
-            if (COMP) v[i] = mul2(strength(gi, a[i]), v[i]);
+    Seq seq = {0, 0, 0};
+    float2 carry = both(0.f);  // the state that enters the cluster's step (the last warp's)
+    for (int step = 0; step < u.steps; ++step, first += cluster * u.tile) {
+        // first pass: the map of the warp's tokens
+        const Seq begin = seq;
+        const bool plain = inside(p, u, seq, first, M * kSpan);
+        float4 own = make_float4(1.f, 0.f, 1.f, 0.f);
+        bool cuts = false;
+        if (plain) {
+            for (int k = 0; k < M; ++k) {
+                copy_wait(M - 1 - k);
+                __syncwarp();
+                float2 a[kSpan], v[kSpan];
+                load_span<COMP>(reinterpret_cast<const T *>(mine + k * kBytes), reinterpret_cast<const G *>(mine + k * kBytes + kBytesX), lane, a, v);
+                const float4 f = map_span<true>(p, u, a, v, 0, nullptr, c);
+                const float2 Ak = make_float2(f.x, f.z), X = fma2(Ak, make_float2(own.y, own.w), make_float2(f.y, f.w));
+                const float2 A = mul2(Ak, make_float2(own.x, own.z));
+                own = make_float4(A.x, X.x, A.y, X.y);
+            }
+        } else for (int k = 0; k < M; ++k) {
+            const Span s = span_at(p, sh, u, first + k * kSpan, warp, lane, &seq);
+            copy_wait(M - 1 - k);
+            __syncwarp();
+            float2 a[kSpan], v[kSpan];
+            load_span<COMP>(reinterpret_cast<const T *>(mine + k * kBytes), reinterpret_cast<const G *>(mine + k * kBytes + kBytesX), lane, a, v);
+            const float4 f = s.plain ? map_span<true>(p, u, a, v, 0, nullptr, c)
+                                     : map_span<false>(p, u, a, v, s.m.starts, start_of, c);
+            const float2 X = join(f, s.m.starts != 0, make_float2(own.y, own.w));
+            own = make_float4(own.x * f.x, X.x, own.z * f.z, X.y);
+            cuts |= s.m.starts != 0;
         }
-        const float4 own = plain ? map_span<true>(p, u, a, v, 0, nullptr, c)
-                                 : map_span<false>(p, u, a, v, m.starts, start_of, c);
         sh.spans[warp][lane] = own;
-        if (lane == 0) sh.cut[warp] = m.starts != 0;
-        const bool any = __syncthreads_or(m.starts != 0);
-        // the map of the spans before this one
+        if (lane == 0) sh.cut[warp] = cuts;
+        const bool any = __syncthreads_or(cuts);
+        // the map of the warps before this one
         float2 PA = both(1.f), PX = both(0.f);
         bool cut = false;
         if (!any) {
@@ -546,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __gr
                     PA = mul2(PA, make_float2(s.x, s.z));
                 }
         } else {
+#pragma unroll 1
             for (int j = 0; j < warp; ++j) {
                 const float4 s = sh.spans[j][lane];
                 const bool here = sh.cut[j] & 1;
@@ -554,26 +611,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __gr
                 cut |= here;
             }
         }
-        float4 q;
-        bool qcut;
         if (warp == kWarps - 1) {
-            const float2 X = join(own, m.starts != 0, PX);
-            q = make_float4(PA.x * own.x, X.x, PA.y * own.z, X.y);
-            qcut = cut || m.starts != 0;
-            send_map(p, sh, u.rank, step, lane, q, qcut);
+            const float2 X = join(own, cuts, PX);
+            const float4 q = make_float4(PA.x * own.x, X.x, PA.y * own.z, X.y);
+            send_map(p, sh, maps, u.rank, step, lane, q, cut || cuts);
+            carry_on<false>(p, sh, maps, u.rank, step, lane, q, cut || cuts, &carry);
         }
-        fetch(step + stages, stage);
-        next = marks(step + 1);
-        if (warp == kWarps - 1) carry_on<false>(p, sh, u.rank, step, lane, q, qcut, &carry);
         __syncthreads();
         if (sh.dead) break;
-        const float2 h = cut ? PX : fma2(PA, sh.enter[lane], PX);
-        if (p.states && at % kSaved == 0 && count)
-            store_state(p.states, (u.saved0 + at / kSaved) * p.D + c, h, u.mine);
-        if (plain)
-            run_span<true, EVEN>(p, u, a, v, h, m, count, start_of, end_of, c, o ? o + at * p.os : nullptr);
-        else
-            run_span<false, EVEN>(p, u, a, v, h, m, count, start_of, end_of, c, o ? o + at * p.os : nullptr);
+        float2 h = cut ? PX : fma2(PA, sh.enter[lane], PX);
+        // second pass: the tokens, and the next step's in their place
+        seq = begin;
+        T *o = static_cast<T *>(p.o) + ((int64_t)u.tok0 + first) * p.os + c;
+        uint32_t save = p.states ? (first + p.saved_every - 1) / p.saved_every : 0;  // the next saved state
+        for (int k = 0; k < M; ++k, o += kSpan * p.os) {
+            const uint32_t t0 = first + k * kSpan;
+            if (p.states && t0 == save * p.saved_every) {
+                if (t0 < (uint32_t)u.S) store_state(p.states, (int64_t)(u.saved0 + save) * p.D + c, h, u.mine);
+                ++save;
+            }
+            Span s;
+            if (plain)
+                s.t0 = t0, s.count = kSpan, s.m = Marks{0, 0}, s.plain = true;
+            else
+                s = span_at(p, sh, u, t0, warp, lane, &seq);
+            float2 a[kSpan], v[kSpan];
+            load_span<COMP>(reinterpret_cast<const T *>(mine + k * kBytes), reinterpret_cast<const G *>(mine + k * kBytes + kBytesX), lane, a, v);
+            if (s.plain)
+                h = run_span<true, ALIGNED>(p, u, a, v, h, s, start_of, end_of, c, o);
+            else
+                h = run_span<false, ALIGNED>(p, u, a, v, h, s, start_of, end_of, c, o);
+            __syncwarp();
+            if (step + 1 < u.steps) fetch(first + cluster * u.tile + k * kSpan, k);
+        }
     }
     copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
@@ -581,138 +651,127 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __gr
 }
 
 // ---------------------------------------------------------------- backward
-// A token's two channels as they are kept in registers.
-__device__ __forceinline__ float2 raw(const float *p, int lane) { return load2(p, lane); }
-__device__ __forceinline__ __nv_bfloat162 raw(const __nv_bfloat16 *p, int lane) {
-    return reinterpret_cast<const __nv_bfloat162 *>(p)[lane];
-}
-__device__ __forceinline__ float2 value(float2 v) { return v; }
-__device__ __forceinline__ float2 value(__nv_bfloat162 v) { return __bfloat1622float2(v); }
-
-// The reverse map of a span.
-template <bool PLAIN, int kSpan, typename R>
-__device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                           const R (&d)[kSpan], uint32_t ends, const int *end_of, int64_t c) {
+// The reverse map of a span; d: its tokens' gradients in shared memory.
+template <bool PLAIN, typename T>
+__device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan], const T *d,
+                                           int lane, uint32_t ends, const int *end_of, int c) {
     float2 Y = both(0.f);
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
         if (!PLAIN && (ends >> i & 1)) Y = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
-        Y = mul2(a[i], add2(value(d[i]), Y));
+        Y = mul2(a[i], add2(load2(d + i * kCh, lane), Y));
     }
     return Y;
 }
 
 // The span's tokens: the states before them, then the gradients from the last to the first.
-template <bool PLAIN, bool COMP, bool EVEN, int kSpan, typename R, typename T, typename G>
-__device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                         const float2 (&w)[kSpan], const R (&x)[kSpan], const R (&d)[kSpan], float2 h,
-                                         float2 r, Marks m, int count, const int *start_of, const int *end_of,
-                                         int64_t c, T *dx, G *dg) {
-    float2 before[kSpan];
+template <bool PLAIN, bool COMP, bool EVEN, typename T, typename G>
+__device__ __forceinline__ float2 run_back(const LinrecParams &p, const Unit &u, const T *x, const T *d, const G *g,
+                                           int lane, float2 h, float2 r, const Span &s, const int *start_of,
+                                           const int *end_of, int c, T *dx, G *dg) {
+    float2 a[kSpan], w[kSpan], before[kSpan];
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
-        if (!PLAIN && (m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
-        const float2 v = value(x[i]);
-        before[i] = COMP ? make_float2(h.x - v.x, h.y - v.y) : h;
+        const float2 gi = load2(g + i * kCh, lane), v = load2(x + i * kCh, lane);
+        a[i] = decay(gi);
+        w[i] = COMP ? strength(gi, a[i]) : both(1.f);
+        if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        before[i] = COMP ? fma2(v, both(-1.f), h) : h;
         h = fma2(a[i], h, COMP ? mul2(w[i], v) : v);
     }
+    dx += (kSpan - 1) * p.dxs;
+    dg += (kSpan - 1) * p.dgs;
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
-        if (!PLAIN && (m.ends >> i & 1)) r = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
-        const float2 e = add2(value(d[i]), r);
+        if (!PLAIN && (s.m.ends >> i & 1)) r = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
+        const float2 e = add2(load2(d + i * kCh, lane), r);
         r = mul2(a[i], e);
-        if (PLAIN || i < count) {
-            store_pair<EVEN>(dx + i * p.dxs, COMP ? mul2(w[i], e) : e, u.mine);
-            store_pair<EVEN>(dg + i * p.dgs, mul2(r, before[i]), u.mine);
+        if (PLAIN || i < s.count) {
+            store_pair<EVEN>(dx, COMP ? mul2(w[i], e) : e, u.mine);
+            store_pair<EVEN>(dg, mul2(r, before[i]), u.mine);
         }
-        if (!PLAIN && (m.starts >> i & 1)) store_state(p.dh0, start_of[i] * p.D + c, r, u.mine);
+        dx -= p.dxs;
+        dg -= p.dgs;
+        if (!PLAIN && (s.m.starts >> i & 1)) store_state(p.dh0, start_of[i] * p.D + c, r, u.mine);
     }
+    return r;
 }
 
-template <int kSpan, typename T, typename G, bool COMP, bool EVEN>
-__global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
-    extern __shared__ __align__(16) unsigned char smem[];
+template <typename T, typename G, bool COMP, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
+    extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Shared sh;
-    constexpr int kTile = kSpan * kWarps;
-    static_assert(kTile == kSaved, "a tile starts from a saved state");
-    constexpr int kRowsX = kSpan * kCh * sizeof(T), kRows = 2 * kRowsX + kSpan * kCh * sizeof(G);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, stages = p.stages;
-    const Unit u = unit_of(p, kTile, lane);
-    const int64_t c = u.c0 + 2 * lane;
+    constexpr int kBytesX = kSpan * kCh * sizeof(T), kBytes = 2 * kBytesX + kSpan * kCh * sizeof(G);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, M = p.spans;
+    const Unit u = unit_of(p, lane);
+    const int c = u.c0 + 2 * lane;
+    unsigned char *mine = smem + warp * M * kBytes;
+    float4 *own_maps = reinterpret_cast<float4 *>(smem + kWarps * M * kBytes) + warp * M * 32 + lane;  // of the warp's spans
+    Map *maps = reinterpret_cast<Map *>(smem + kWarps * M * (kBytes + 32 * sizeof(float4)));
+    const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
     cluster_begin(sh, cluster);
 
-    unsigned char *mine = smem + (size_t)warp * stages * kRows;
-    const T *x = static_cast<const T *>(p.x) + u.tok0 * p.xs + u.c0;
-    const T *dy = static_cast<const T *>(p.dy) + u.tok0 * p.os + u.c0;
-    const G *g = static_cast<const G *>(p.g) + u.tok0 * p.gs + u.c0;
-    T *dx = static_cast<T *>(p.dx) + u.tok0 * p.dxs + c;
-    G *dg = static_cast<G *>(p.dg) + u.tok0 * p.dgs + c;
-    // steps count from the stream's end
-    const auto first_token = [&](int step) {
-        return ((int64_t)(u.steps - 1 - step) * cluster + u.rank) * kTile + warp * kSpan;
-    };
-    const auto fetch = [&](int step, int stage) {
-        if (step < u.steps) {
-            const int64_t t0 = first_token(step);
-            const int rows = t0 >= u.S ? 0 : u.S - t0 < kSpan ? (int)(u.S - t0) : kSpan;
-            unsigned char *to = mine + stage * kRows;
-            copy_rows<kSpan>(reinterpret_cast<T *>(to), rows ? x + t0 * p.xs : x, p.xs, rows, u.cols, p.wide, p.even, lane);
-            copy_rows<kSpan>(reinterpret_cast<T *>(to + kRowsX), rows ? dy + t0 * p.os : dy, p.os, rows, u.cols, p.wide, p.even, lane);
-            copy_rows<kSpan>(reinterpret_cast<G *>(to + 2 * kRowsX), rows ? g + t0 * p.gs : g, p.gs, rows, u.cols, p.wide, p.even, lane);
-        }
+    const auto fetch = [&](uint32_t t0, int k) {
+        const int rows = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
+        const int64_t tok = (int64_t)u.tok0 + (rows ? t0 : 0);
+        T *x = reinterpret_cast<T *>(mine + k * kBytes), *d = reinterpret_cast<T *>(mine + k * kBytes + kBytesX);
+        G *g = reinterpret_cast<G *>(mine + k * kBytes + 2 * kBytesX);
+        copy_rows<ALIGNED>(x, static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
+        copy_rows<ALIGNED>(d, static_cast<const T *>(p.dy) + tok * p.os + u.c0, p.os, rows, u.cols, p.even, lane);
+        copy_rows<ALIGNED>(g, static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
         copy_commit();
     };
-    Seq seq = {0, 0, 0};
-    const auto marks = [&](int step) {
-        if (step >= u.steps) return Marks{0, 0};
-        const int64_t at = first_token(step);
-        const int t0 = at < u.S ? (int)at : u.S, t1 = u.S - t0 < kSpan ? u.S : t0 + kSpan;
-        return mark(p, u.first, u.S, t0, t1, lane, &seq, sh.start_of[step & 1][warp], sh.end_of[step & 1][warp]);
-    };
-    // the state that enters a step's tile (the stream's first tile starts a sequence)
-    const auto saved = [&](int step) {
-        const int64_t tile = step < u.steps ? (first_token(step) - warp * kSpan) / kTile : 0;
-        return tile > 0 && tile < p.saved ? load_state(p.states, (u.saved0 + tile) * p.D + c, u.mine) : both(0.f);
-    };
-    for (int i = 0; i < stages; ++i) fetch(i, i);
-    Marks next = marks(0);
-    float2 enter = saved(0);
-    float2 carry = both(0.f);  // the gradient of the state that leaves the step (the first warp's)
+    // steps go from the stream's end, spans from the warp's last
+    uint32_t tile = ((uint32_t)(u.steps - 1) * cluster + u.rank) * u.tile;
+    for (int k = M - 1; k >= 0; --k) fetch(tile + (warp * M + k) * kSpan, k);
     cluster_ready(cluster);
 
-    for (int step = 0, stage = 0; step < u.steps; ++step, stage = stage + 1 == stages ? 0 : stage + 1) {
-        const Marks m = next;
-        const int *start_of = sh.start_of[step & 1][warp], *end_of = sh.end_of[step & 1][warp];
-        const int64_t at = first_token(step);
-        const int count = at >= u.S ? 0 : u.S - at < kSpan ? (int)(u.S - at) : kSpan;
-        const bool plain = !(m.starts | m.ends) && count == kSpan;
-        copy_wait(stages - 1);
-        __syncwarp();
-        float2 a[kSpan], w[kSpan];
-        decltype(raw((const T *)nullptr, 0)) xv[kSpan], dv[kSpan];
-        const T *xr = reinterpret_cast<const T *>(mine + stage * kRows);
-        const T *dr = reinterpret_cast<const T *>(mine + stage * kRows + kRowsX);
-        const G *gr = reinterpret_cast<const G *>(mine + stage * kRows + 2 * kRowsX);
-        float2 v[kSpan];
-#pragma unroll
-        for (int i = 0; i < kSpan; ++i) {
-            const float2 gi = load2(gr + i * kCh, lane);
-            a[i] = decay(gi);
-            w[i] = COMP ? strength(gi, a[i]) : both(1.f);
-            xv[i] = raw(xr + i * kCh, lane);
-            dv[i] = raw(dr + i * kCh, lane);
-            v[i] = COMP ? mul2(w[i], value(xv[i])) : value(xv[i]);
+    Seq seq = {0, 0, 0};
+    float2 carry = both(0.f);  // the gradient of the state that leaves the step (the first warp's)
+    for (int step = 0; step < u.steps; ++step, tile -= cluster * u.tile) {
+        const uint32_t first = tile + warp * M * kSpan;
+        // the state that enters the tile (the stream's first tile starts a sequence)
+        float2 h = both(0.f);
+        if (tile > 0 && tile < (uint32_t)u.S) h = load_state(p.states, (int64_t)(u.saved0 + tile / u.tile) * p.D + c, u.mine);
+        // first pass: the maps of the warp's tokens in both directions
+        const Seq begin = seq;
+        const bool plain = inside(p, u, seq, first, M * kSpan);
+        float2 A = both(1.f), X = both(0.f), Y = both(0.f);
+        bool starts = false, ends = false;
+        for (int k = M - 1; k >= 0; --k) {
+            Span s;
+            if (plain)
+                s.plain = true, s.m = Marks{0, 0};
+            else
+                s = span_at(p, sh, u, first + k * kSpan, warp, lane, &seq);
+            copy_wait(k);
+            __syncwarp();
+            const T *xs = reinterpret_cast<const T *>(mine + k * kBytes), *ds = reinterpret_cast<const T *>(mine + k * kBytes + kBytesX);
+            const G *gs = reinterpret_cast<const G *>(mine + k * kBytes + 2 * kBytesX);
+            float2 a[kSpan], v[kSpan], Yk;
+            load_span<COMP>(xs, gs, lane, a, v);
+            float4 f;
+            if (s.plain) {
+                f = map_span<true>(p, u, a, v, 0, nullptr, c);
+                Yk = map_back<true>(p, u, a, ds, lane, 0, end_of, c);
+            } else {
+                f = map_span<false>(p, u, a, v, s.m.starts, start_of, c);
+                Yk = map_back<false>(p, u, a, ds, lane, s.m.ends, end_of, c);
+            }
+            own_maps[k * 32] = f;
+            const float2 Ak = make_float2(f.x, f.z);
+            if (!starts) X = fma2(A, make_float2(f.y, f.w), X);
+            Y = s.m.ends ? Yk : fma2(Ak, Y, Yk);
+            A = mul2(A, Ak);
+            starts |= s.m.starts != 0;
+            ends |= s.m.ends != 0;
         }
-        const float4 f = plain ? map_span<true>(p, u, a, v, 0, nullptr, c)
-                               : map_span<false>(p, u, a, v, m.starts, start_of, c);
-        const float2 Y = plain ? map_back<true>(p, u, a, dv, 0, nullptr, c)
-                               : map_back<false>(p, u, a, dv, m.ends, end_of, c);
-        const float4 own = make_float4(f.x, Y.x, f.z, Y.y);
+        const float4 own = make_float4(A.x, Y.x, A.y, Y.y);
         sh.spans[warp][lane] = own;
-        sh.starts[warp][lane] = make_float2(f.y, f.w);
-        if (lane == 0) sh.cut[warp] = (m.starts != 0) | (m.ends != 0) << 1;
+        sh.starts[warp][lane] = X;
+        if (lane == 0) sh.cut[warp] = starts | ends << 1;
         __syncthreads();
-        // the reverse map of the spans after this one
+        // the reverse map of the warps after this one
         float2 PA = both(1.f), PY = both(0.f);
         bool cut = false;
 #pragma unroll
@@ -724,34 +783,50 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __gr
                 PA = mul2(PA, make_float2(s.x, s.z));
                 cut |= here;
             }
-        float4 q;
-        bool qcut;
         if (warp == 0) {
-            const float2 R = join(own, m.ends != 0, PY);
-            q = make_float4(PA.x * own.x, R.x, PA.y * own.z, R.y);
-            qcut = cut || m.ends != 0;
-            send_map(p, sh, u.rank, step, lane, q, qcut);
+            const float2 R = join(own, ends, PY);
+            const float4 q = make_float4(PA.x * own.x, R.x, PA.y * own.z, R.y);
+            send_map(p, sh, maps, u.rank, step, lane, q, cut || ends);
+            carry_on<true>(p, sh, maps, u.rank, step, lane, q, cut || ends, &carry);
         }
-        fetch(step + stages, stage);
-        next = marks(step + 1);
-        // the state that enters the span
-        float2 h = enter;
-        enter = saved(step + 1);
+        // the states that enter the warp's spans, in place of the spans' own
 #pragma unroll
         for (int j = 0; j < kWarps - 1; ++j)
             if (j < warp) {
                 const float4 s = sh.spans[j][lane];
-                const float2 X = sh.starts[j][lane];
-                h = sh.cut[j] & 1 ? X : fma2(make_float2(s.x, s.z), h, X);
+                const float2 Xj = sh.starts[j][lane];
+                h = sh.cut[j] & 1 ? Xj : fma2(make_float2(s.x, s.z), h, Xj);
             }
-        if (warp == 0) carry_on<true>(p, sh, u.rank, step, lane, q, qcut, &carry);
+        seq = begin;
+        for (int k = 0; k < M - 1; ++k) {
+            const float4 f = own_maps[k * 32];
+            own_maps[k * 32] = make_float4(h.x, h.y, 0.f, 0.f);
+            // a start in the span: its X is the state that leaves it
+            h = !plain && span_at(p, sh, u, first + k * kSpan, warp, lane, &seq).m.starts ? make_float2(f.y, f.w) : fma2(make_float2(f.x, f.z), h, make_float2(f.y, f.w));
+        }
+        own_maps[(M - 1) * 32] = make_float4(h.x, h.y, 0.f, 0.f);
         __syncthreads();
         if (sh.dead) break;
-        const float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
-        if (plain)
-            run_back<true, COMP, EVEN>(p, u, a, w, xv, dv, h, r, m, count, start_of, end_of, c, dx + at * p.dxs, dg + at * p.dgs);
-        else
-            run_back<false, COMP, EVEN>(p, u, a, w, xv, dv, h, r, m, count, start_of, end_of, c, dx + at * p.dxs, dg + at * p.dgs);
+        float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
+        // second pass: the tokens, and the next step's in their place
+        for (int k = M - 1; k >= 0; --k) {
+            Span s;
+            if (plain)
+                s.t0 = first + k * kSpan, s.count = kSpan, s.m = Marks{0, 0}, s.plain = true;
+            else
+                s = span_at(p, sh, u, first + k * kSpan, warp, lane, &seq);
+            const T *xs = reinterpret_cast<const T *>(mine + k * kBytes), *ds = reinterpret_cast<const T *>(mine + k * kBytes + kBytesX);
+            const G *gs = reinterpret_cast<const G *>(mine + k * kBytes + 2 * kBytesX);
+            const float4 e = own_maps[k * 32];
+            T *dx = static_cast<T *>(p.dx) + ((int64_t)u.tok0 + s.t0) * p.dxs + c;
+            G *dg = static_cast<G *>(p.dg) + ((int64_t)u.tok0 + s.t0) * p.dgs + c;
+            if (s.plain)
+                r = run_back<true, COMP, ALIGNED>(p, u, xs, ds, gs, lane, make_float2(e.x, e.y), r, s, start_of, end_of, c, dx, dg);
+            else
+                r = run_back<false, COMP, ALIGNED>(p, u, xs, ds, gs, lane, make_float2(e.x, e.y), r, s, start_of, end_of, c, dx, dg);
+            __syncwarp();
+            if (step + 1 < u.steps) fetch(tile - cluster * u.tile + (warp * M + k) * kSpan, k);
+        }
     }
     copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
@@ -791,7 +866,7 @@ cudaError_t launch_cluster(void (*kernel)(LinrecParams), std::atomic<uint64_t> *
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (dev > 63 || !(ready->load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemSm - kSmemCta));
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         ready->fetch_or(bit, std::memory_order_relaxed);
@@ -810,39 +885,46 @@ cudaError_t launch_cluster(void (*kernel)(LinrecParams), std::atomic<uint64_t> *
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Tokens per warp: 16 in the forward of bf16 inputs, whose factors and inputs then take 64
-// registers and whose tiles 32 or 48 KB; 8 where a tile of 16 would not leave room for two CTAs
-// and a second stage.
-template <typename T> constexpr int kFwdSpan = sizeof(T) == 2 ? 16 : 8;
-constexpr int kBwdSpan = 8;
+// CTAs that run at once, two or three per SM, in clusters of 1, 2, 4, 8 and 16
+// (cudaOccupancyMaxActiveClusters on a B200: clusters stay within a group of SMs).
+int64_t capacity(int per_sm, int cluster) {
+    static const int kCtas[2][5] = {{296, 296, 284, 264, 224}, {444, 444, 416, 384, 336}};
+    int i = 0;
+    while (1 << i < cluster) ++i;
+    return kCtas[per_sm - 2][i];
+}
 
-template <typename T, typename G, bool COMP, bool EVEN>
+// The cluster and the spans per warp for streams of p: the longest clusters that can all run at
+// once and that the stream fills; then as many spans as the stream gives its CTAs and their shared
+// memory holds.
+void plan(const LinrecParams &p, size_t span_bytes, int per_sm, int32_t *cluster, int32_t *spans) {
+    const int64_t rows = (p.rows_per_stream * p.T + kRows - 1) / kRows, units = p.streams * p.slabs;
+    int k = 1;
+    while (k < kMaxCluster && k < rows && units * k * 2 <= capacity(per_sm, k * 2)) k *= 2;
+    const size_t room = kSmemSm / per_sm - kSmemCta - (k > 1 ? 2 * k * sizeof(Map) : 0);
+    int64_t m = (int64_t)(room / (kWarps * span_bytes));
+    if (m > kMaxSpans) m = kMaxSpans;
+    if (m > (rows + k - 1) / k) m = (rows + k - 1) / k;
+    *cluster = k;
+    *spans = m < 1 ? 1 : (int32_t)m;
+}
+size_t fwd_span_bytes(int es, int ges) { return (size_t)kSpan * kCh * (es + ges); }
+size_t bwd_span_bytes(int es, int ges) { return (size_t)kSpan * kCh * (2 * es + ges) + 32 * sizeof(float4); }
+
+template <typename T, typename G, bool COMP, bool ALIGNED>
 cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
     static std::atomic<uint64_t> ready[2];
     const bool fwd = pass == Pass::kFwd;
-    const int64_t tile = kWarps * (fwd ? kFwdSpan<T> : kBwdSpan);
-    const size_t bytes = tile * kCh * (fwd ? sizeof(T) + sizeof(G) : 2 * sizeof(T) + sizeof(G));
-    const int64_t tiles = (p.rows_per_stream * p.T + tile - 1) / tile;
-    // CTAs: as many as give every SM kPerSm of them, in clusters no longer than the stream
-    const int64_t units = p.streams * p.slabs;
-    p.cluster = 1;
-    while (p.cluster < kMaxCluster && 2 * p.cluster <= tiles && units * p.cluster * 2 <= kSms * kPerSm) p.cluster *= 2;
-    // stages: what the SM's shared memory holds for the CTAs that it gets, up to the steps there are
-    const int64_t per_sm = (units * p.cluster + kSms - 1) / kSms;
-    const int64_t steps = (tiles + p.cluster - 1) / p.cluster;
-    const size_t room = kSmemSm / (per_sm < 1 ? 1 : per_sm > kPerSm ? kPerSm : per_sm) - kSmemStatic - 1024;
-    int64_t stages = (int64_t)((room < kSmemMax ? room : kSmemMax) / bytes);
-    if (stages > kMaxStages) stages = kMaxStages;
-    if (stages > steps) stages = steps;
-    p.stages = stages < 1 ? 1 : (int32_t)stages;
-    const size_t smem = bytes * p.stages;
+    const size_t bytes = fwd ? fwd_span_bytes(sizeof(T), sizeof(G)) : bwd_span_bytes(sizeof(T), sizeof(G));
+    plan(p, bytes, fwd ? kFwdPerSm : kBwdPerSm, &p.cluster, &p.spans);
+    const size_t smem = kWarps * p.spans * bytes + (p.cluster > 1 ? 2 * p.cluster * sizeof(Map) : 0);
     p.wait_limit = call_wait_limit();
     p.test_hook = call_test_hook();
     cudaError_t err = cudaSuccess;
     if (fwd)
-        GDN_LAUNCH(kKLinrecFwd, s, (err = launch_cluster(linrec_fwd_kernel<kFwdSpan<T>, T, G, COMP, EVEN>, &ready[0], p, smem, s)));
+        GDN_LAUNCH(kKLinrecFwd, s, (err = launch_cluster(linrec_fwd_kernel<T, G, COMP, ALIGNED>, &ready[0], p, smem, s)));
     else
-        GDN_LAUNCH(kKLinrecBwd, s, (err = launch_cluster(linrec_bwd_kernel<kBwdSpan, T, G, COMP, EVEN>, &ready[1], p, smem, s)));
+        GDN_LAUNCH(kKLinrecBwd, s, (err = launch_cluster(linrec_bwd_kernel<T, G, COMP, ALIGNED>, &ready[1], p, smem, s)));
     return err;
 }
 
@@ -853,7 +935,7 @@ cudaError_t launch_even(const LinrecParams &p, Pass pass, float *state, cudaStre
         GDN_LAUNCH(kKLinrecDecode, s, linrec_decode_kernel<T, G, COMP><<<grid, 128, 0, s>>>(p, state));
         return cudaSuccess;
     }
-    return p.even ? launch_typed<T, G, COMP, true>(p, pass, s) : launch_typed<T, G, COMP, false>(p, pass, s);
+    return p.aligned ? launch_typed<T, G, COMP, true>(p, pass, s) : launch_typed<T, G, COMP, false>(p, pass, s);
 }
 
 template <typename T, typename G>
@@ -862,13 +944,11 @@ cudaError_t launch_comp(const LinrecParams &p, bool comp, Pass pass, float *stat
 }
 
 cudaError_t launch(const gdn_linrec_desc *d, LinrecParams p, Pass pass, float *state, cudaStream_t s) {
-    // 16-byte copies need rows that start on 16 bytes; pairs of channels need even rows
+    // 16-byte copies need rows that start on 16 bytes; pairs of channels even rows.
+    const bool bwd = pass == Pass::kBwd;
     const int es = d->dtype == GDN_BF16 ? 2 : 4, ges = d->g_dtype == GDN_BF16 ? 2 : 4;
-    const int64_t in[] = {p.xs * es, p.gs * ges, pass == Pass::kBwd ? p.os * es : 0};
-    p.wide = 1;
-    for (int64_t b : in)
-        if (b % 16) p.wide = 0;
-    p.even = (p.D | p.xs | p.gs | p.os) % 2 == 0 && (pass != Pass::kBwd || (p.dxs | p.dgs) % 2 == 0);
+    p.even = (p.D | p.xs | p.gs | p.os) % 2 == 0 && (!bwd || (p.dxs | p.dgs) % 2 == 0);
+    p.aligned = p.even && p.xs * es % 16 == 0 && p.gs * ges % 16 == 0 && (!bwd || p.os * es % 16 == 0);
     const bool comp = d->flags & GDN_LINREC_COMPLEMENT;
     if (d->dtype == GDN_FP32) return launch_comp<float, float>(p, comp, pass, state, s);
     if (d->g_dtype == GDN_FP32) return launch_comp<__nv_bfloat16, float>(p, comp, pass, state, s);
@@ -900,11 +980,16 @@ gdn_status describe(const gdn_linrec_desc *d, LinrecParams *p) {
     p->D = d->D;
     p->N = d->n_seqs > 0 ? d->n_seqs : d->B;
     // streams: the packed row, a dense row, or as many short dense rows as fill a tile
-    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kSaved ? kSaved / p->T : 1;
+    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kRows ? kRows / p->T : 1;
     p->streams = d->n_seqs > 0 ? 1 : (p->N + p->rows_per_stream - 1) / p->rows_per_stream;
-    p->saved = (p->rows_per_stream * p->T + kSaved - 1) / kSaved;
+    p->single = d->n_seqs > 0 ? d->n_seqs == 1 : p->rows_per_stream == 1;
     p->slabs = (int32_t)((p->D + kCh - 1) / kCh);
     if (p->streams * p->slabs >= kLim / kMaxCluster) return GDN_ERR_INVALID_ARG;
+    // a saved state for every tile of the backward
+    int32_t cluster, spans;
+    plan(*p, bwd_span_bytes(d->dtype == GDN_BF16 ? 2 : 4, d->g_dtype == GDN_BF16 ? 2 : 4), kBwdPerSm, &cluster, &spans);
+    p->saved_every = kRows * spans;
+    p->saved = (p->rows_per_stream * p->T + p->saved_every - 1) / p->saved_every;
     const int64_t in[] = {d->x_stride, d->g_stride, d->o_stride, d->dx_stride, d->dg_stride};
     int64_t *out[] = {&p->xs, &p->gs, &p->os, &p->dxs, &p->dgs};
     for (int i = 0; i < 5; ++i) {
