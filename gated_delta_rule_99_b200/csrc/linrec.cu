@@ -4,25 +4,25 @@
 // A sequence's map over any span of tokens is affine per channel, h' = A h + X with
 // A the product of the span's factors, and the reverse map of the gradients is
 // r' = A r + Y with the same A; spans join by (A2, X2)(A1, X1) = (A2 A1, A2 X1 + X2).
-// A CTA takes 64 channels (two per lane) and a tile of 64 M tokens at a time, 8 M adjacent
-// tokens per warp, which stay in shared memory through two passes: the first forms the
-// warp's map, the second runs its tokens from the state that enters them and refills each
-// 8 tokens' place with the next tile's, so copies are on their way during the second pass.
-// In between, the warps join the maps before theirs; the last one, which thereby has the
+// A CTA takes 64 channels (two per lane) and a tile of adjacent tokens at a time, split into
+// one span per warp, whose factors and inputs stay in registers.  Each of eight warps forms its
+// span's map and joins the maps of the spans before it; the last one, which thereby has the
 // tile's map, carries the state.  A cluster of up to 16 CTAs takes consecutive tiles of the
 // same channels: the carrying warps send their tile's map to all of them (one bulk copy each
 // through distributed shared memory, counted by an mbarrier: a cluster barrier's release
 // would wait for the outputs still being stored) and each folds them in order, so each holds
-// the state that enters its tile and the next step.  The data is read from memory once.
+// the state that enters its tile and the next step.  The data is read from memory once, by
+// cp.async into a ring of tiles that runs ahead of the steps, each warp copying its own rows.
 //
 // A start of a sequence inside a span drops what comes before it by selection (not by a
 // factor of 0), so that no infinity or NaN crosses; padded tokens are zeros (factor
 // exp(0) = 1, input 0), which is the identity map in both directions.
 //
 // The backward runs the tiles from the last to the first.  It needs the states that
-// enter each token: the forward leaves the state entering every tile of the backward (at
-// most 4 / 64 bytes per element), from which a tile recomputes its own.
+// enter each token: the forward leaves the state entering every 64th token (4 / 64 bytes per
+// element), from which a tile recomputes its own.
 #include <atomic>
+#include <mutex>
 #include <vector>
 
 #include "gdn_internal.cuh"
@@ -33,21 +33,23 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSpan = 8;       // adjacent tokens that a warp has in registers at a time
-constexpr int kRows = kSpan * kWarps;
 constexpr int kCh = 64;        // channels per CTA
-constexpr int kMaxSpans = 8;   // M: spans per warp and tile
-constexpr int kMaxCluster = 16;
-constexpr int kSms = 148, kFwdPerSm = 3, kBwdPerSm = 2;  // CTAs per SM that the registers allow
-constexpr size_t kSmemSm = 227 * 1024, kSmemCta = 9 * 1024 + 256;  // of an SM, and of a CTA beside tiles and maps
+constexpr int kSaved = 64;     // tokens between two saved states
+constexpr int kMaxSpan = 16, kMaxStages = 8, kMaxCluster = 16;
+constexpr int kSms = 148, kFwdPerSm = 2, kBwdPerSm = 2;  // CTAs per SM that the registers allow
+constexpr size_t kSmemSm = 227 * 1024, kSmemCta = 9 * 1024 + 512;  // of an SM, and of a CTA beside tiles and maps
+
+// Tokens per warp: 16 in the forward of bf16 inputs; 8 where the tiles are larger, and in the
+// backward, which has more to keep in registers.
+template <typename T> constexpr int kFwdSpan = sizeof(T) == 2 ? 16 : 8;
+constexpr int kBwdSpan = 8;
 
 struct LinrecParams {
     int64_t T, BT, D, N;
     int64_t xs, gs, os, dxs, dgs;
     int64_t streams, rows_per_stream;  // a stream: one dense row, several short ones, or the packed row
     int64_t saved;                            // saved states of a stream
-    int32_t saved_every;                      // tokens between two of them
-    int32_t slabs, cluster, spans, aligned, even;
+    int32_t slabs, cluster, stages, aligned, even;
     uint32_t wait_limit;
     int32_t test_hook;
     int32_t single;  // every stream is one sequence
@@ -92,24 +94,10 @@ __device__ __forceinline__ void store_state(float *p, int64_t at, float2 v, int 
     if (p && n > 0) p[at] = v.x;
     if (p && n > 1) p[at + 1] = v.y;
 }
-// Two lanes' worth of fp32 arithmetic per instruction.
-__device__ __forceinline__ uint64_t bits(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
-__device__ __forceinline__ float2 pair(uint64_t b) { return *reinterpret_cast<float2 *>(&b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return pair(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return pair(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return pair(d);
-}
+__device__ __forceinline__ float2 pfma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ float exp_base2(float x) {
@@ -126,13 +114,13 @@ __device__ __forceinline__ float2 decay(float2 g) {
 // (the next term is below 2^-26 of the sum), beyond it the difference.
 __device__ __forceinline__ float2 strength(float2 g, float2 a) {
     float2 s = both(-1.f / 40320);
-    s = fma2(s, g, both(-1.f / 5040));
-    s = fma2(s, g, both(-1.f / 720));
-    s = fma2(s, g, both(-1.f / 120));
-    s = fma2(s, g, both(-1.f / 24));
-    s = fma2(s, g, both(-1.f / 6));
-    s = fma2(s, g, both(-1.f / 2));
-    s = fma2(s, g, both(-1.f));
+    s = pfma2(s, g, both(-1.f / 5040));
+    s = pfma2(s, g, both(-1.f / 720));
+    s = pfma2(s, g, both(-1.f / 120));
+    s = pfma2(s, g, both(-1.f / 24));
+    s = pfma2(s, g, both(-1.f / 6));
+    s = pfma2(s, g, both(-1.f / 2));
+    s = pfma2(s, g, both(-1.f));
     s = mul2(s, g);
     return make_float2(fabsf(g.x) <= 0.5f ? s.x : 1.f - a.x, fabsf(g.y) <= 0.5f ? s.y : 1.f - a.y);
 }
@@ -164,7 +152,7 @@ __device__ __forceinline__ void copy_wait(int pending) {
 // A span's tokens x 64 channels; `rows` and `cols` of them exist, the rest become zeros.  Rows that
 // start on 16 bytes: 16 at a time (the last ones maybe in part); fp32, or bf16 with even rows: 4 at
 // a time; else one bf16 after another.
-template <bool ALIGNED, typename E>
+template <int kSpan, bool ALIGNED, typename E>
 __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, int rows, int cols,
                                           int even, int lane) {
     if (ALIGNED) {
@@ -318,13 +306,12 @@ struct Unit {
     int first;   // first sequence of the stream (dense)
     int tok0;    // the stream's first token
     int saved0;  // its first saved state
-    int tile;    // tokens of a CTA and step
     int S, steps;  // its tokens, and the cluster's steps over them
     int c0;
     int cols, mine;  // channels of the CTA, and of this lane (0, 1 or 2)
     int rank;
 };
-__device__ __forceinline__ Unit unit_of(const LinrecParams &p, int lane) {
+__device__ __forceinline__ Unit unit_of(const LinrecParams &p, int tile, int lane) {
     Unit u;
     u.rank = blockIdx.x % p.cluster;
     const int i = blockIdx.x / p.cluster, stream = i / p.slabs;
@@ -342,8 +329,7 @@ __device__ __forceinline__ Unit unit_of(const LinrecParams &p, int lane) {
         u.S = rows * (int)p.T;
     }
     u.saved0 = stream * (int)p.saved;
-    u.tile = kRows * p.spans;
-    u.steps = (int)((u.S + (int64_t)u.tile * p.cluster - 1) / ((int64_t)u.tile * p.cluster));
+    u.steps = (int)((u.S + (int64_t)tile * p.cluster - 1) / ((int64_t)tile * p.cluster));
     return u;
 }
 
@@ -376,7 +362,7 @@ struct Shared {
     float2 enter[32];                       // what enters the CTA's tile
     uint64_t bar[2];                        // arrivals of the cluster's maps (even, odd steps)
     int cut[kWarps];                        // bit 0: a start in the span, bit 1: an end
-    int start_of[kWarps][kSpan], end_of[kWarps][kSpan];
+    int start_of[kWarps][kMaxSpan], end_of[kWarps][kMaxSpan];
     int dead;                               // a wait ran out
     Map out[2];                             // the tile's map on its way to the cluster (even, odd steps)
 };
@@ -462,33 +448,28 @@ __device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, cons
     *carry = c;
 }
 
-// What a warp's spans of a step are, for both passes.
+// A warp's span of a step.
 struct Span {
-    uint32_t t0;  // first token
-    int count;    // tokens (0 .. 8)
+    int count;  // tokens (0 .. kSpan)
     Marks m;
-    bool plain;   // nothing starts or ends in it, and nothing is missing
+    bool plain;  // nothing starts or ends in it, and nothing is missing
 };
+template <int kSpan>
 __device__ __forceinline__ Span span_at(const LinrecParams &p, Shared &sh, const Unit &u, uint32_t t0, int warp, int lane, Seq *seq) {
-    Span s;
-    s.t0 = t0;
+    Span s = {kSpan, {0, 0}, true};
+    // strictly inside a sequence?
+    if (p.single ? t0 > 0 && t0 + kSpan < (uint32_t)u.S : (int)t0 > seq->beg && t0 + kSpan < (uint32_t)seq->end) return s;
     s.count = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
     __syncwarp();
-    s.m = s.count ? mark(p, u.first, u.S, (int)t0, (int)t0 + s.count, lane, seq, sh.start_of[warp], sh.end_of[warp]) : Marks{0, 0};
+    if (s.count) s.m = mark(p, u.first, u.S, (int)t0, (int)t0 + s.count, lane, seq, sh.start_of[warp], sh.end_of[warp]);
     s.plain = !(s.m.starts | s.m.ends) && s.count == kSpan;
     __syncwarp();
     return s;
 }
 
-// Whether the warp's tokens [t0, t0 + n) of a step lie strictly inside one sequence: nothing starts
-// or ends among them, and none is missing.
-__device__ __forceinline__ bool inside(const LinrecParams &p, const Unit &u, const Seq &s, uint32_t t0, uint32_t n) {
-    return p.single ? t0 > 0 && t0 + n < (uint32_t)u.S : (int)t0 > s.beg && t0 + n < (uint32_t)s.end;
-}
-
 // ---------------------------------------------------------------- forward
 // A span's map.  PLAIN: no sequence starts in it.
-template <bool PLAIN>
+template <bool PLAIN, int kSpan>
 __device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
                                            const float2 (&v)[kSpan], uint32_t starts, const int *start_of, int c) {
     float2 A = a[0], X = v[0];
@@ -502,112 +483,105 @@ __device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u,
     return make_float4(A.x, X.x, A.y, X.y);
 }
 
-// The factors and inputs of a span's tokens from shared memory.
-template <bool COMP, typename T, typename G>
-__device__ __forceinline__ void load_span(const T *x, const G *g, int lane, float2 (&a)[kSpan], float2 (&v)[kSpan]) {
-#pragma unroll
-    for (int i = 0; i < kSpan; ++i) {
-        const float2 gi = load2(g + i * kCh, lane);
-        a[i] = decay(gi);
-        v[i] = load2(x + i * kCh, lane);
-        if (COMP) v[i] = mul2(strength(gi, a[i]), v[i]);
-    }
-}
-
-template <bool PLAIN, bool EVEN, typename T>
-__device__ __forceinline__ float2 run_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                           const float2 (&v)[kSpan], float2 h, const Span &s,
-                                           const int *start_of, const int *end_of, int c, T *o) {
+// Runs the span's tokens from h; `mine` channels are stored (0: only the states are wanted).
+template <bool PLAIN, bool EVEN, int kSpan, typename T>
+__device__ __forceinline__ void run_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                         const float2 (&v)[kSpan], float2 h, const Span &s, int mine,
+                                         const int *start_of, const int *end_of, int c, T *o) {
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
         if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
         h = fma2(a[i], h, v[i]);
-        if (p.o && (PLAIN || i < s.count)) store_pair<EVEN>(o, h, u.mine);
+        if (PLAIN || i < s.count) store_pair<EVEN>(o, h, mine);
         o += p.os;
         if (!PLAIN && (s.m.ends >> i & 1)) store_state(p.hT, end_of[i] * p.D + c, h, u.mine);
     }
-    return h;
 }
 
 // ALIGNED: rows start on 16 bytes, and pairs of channels can be stored at once.
-template <typename T, typename G, bool COMP, bool ALIGNED>
+template <int kSpan, typename T, typename G, bool COMP, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Shared sh;
+    constexpr int kTile = kSpan * kWarps;
     constexpr int kBytesX = kSpan * kCh * sizeof(T), kBytes = kBytesX + kSpan * kCh * sizeof(G);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, M = p.spans;
-    const Unit u = unit_of(p, lane);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, stages = p.stages;
+    const Unit u = unit_of(p, kTile, lane);
     const int c = u.c0 + 2 * lane;
-    unsigned char *mine = smem + warp * M * kBytes;
-    Map *maps = reinterpret_cast<Map *>(smem + kWarps * M * kBytes);
+    unsigned char *mine = smem + warp * stages * kBytes;
+    Map *maps = reinterpret_cast<Map *>(smem + kWarps * stages * kBytes);
     const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
     cluster_begin(sh, cluster);
 
-    const auto fetch = [&](uint32_t t0, int k) {
-        const int rows = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
-        const int64_t tok = (int64_t)u.tok0 + (rows ? t0 : 0);
-        T *x = reinterpret_cast<T *>(mine + k * kBytes);
-        G *g = reinterpret_cast<G *>(mine + k * kBytes + kBytesX);
-        copy_rows<ALIGNED>(x, static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
-        copy_rows<ALIGNED>(g, static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
+    uint32_t t0 = u.rank * kTile + warp * kSpan, ahead = t0;  // the warp's first token of a step, and of the next copies
+    const auto fetch = [&](int stage) {
+        const int rows = ahead >= (uint32_t)u.S ? 0 : u.S - ahead < kSpan ? u.S - ahead : kSpan;
+        if (rows) {
+            const int64_t tok = (int64_t)u.tok0 + ahead;
+            unsigned char *to = mine + stage * kBytes;
+            copy_rows<kSpan, ALIGNED>(reinterpret_cast<T *>(to), static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
+            copy_rows<kSpan, ALIGNED>(reinterpret_cast<G *>(to + kBytesX), static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
+        }
         copy_commit();
+        ahead += cluster * kTile;
     };
-    uint32_t first = u.rank * u.tile + warp * M * kSpan;  // the warp's first token of the step
-    for (int k = 0; k < M; ++k) fetch(first + k * kSpan, k);
+    for (int i = 0; i < stages; ++i) fetch(i);
     cluster_ready(cluster);
 
     Seq seq = {0, 0, 0};
     float2 carry = both(0.f);  // the state that enters the cluster's step (the last warp's)
-    for (int step = 0; step < u.steps; ++step, first += cluster * u.tile) {
-        // first pass: the map of the warp's tokens
-        const Seq begin = seq;
-        const bool plain = inside(p, u, seq, first, M * kSpan);
-        float4 own = make_float4(1.f, 0.f, 1.f, 0.f);
-        bool cuts = false;
-        if (plain) {
-            for (int k = 0; k < M; ++k) {
-                copy_wait(M - 1 - k);
-                __syncwarp();
-                float2 a[kSpan], v[kSpan];
-                load_span<COMP>(reinterpret_cast<const T *>(mine + k * kBytes), reinterpret_cast<const G *>(mine + k * kBytes + kBytesX), lane, a, v);
-                const float4 f = map_span<true>(p, u, a, v, 0, nullptr, c);
-                const float2 Ak = make_float2(f.x, f.z), X = fma2(Ak, make_float2(own.y, own.w), make_float2(f.y, f.w));
-                const float2 A = mul2(Ak, make_float2(own.x, own.z));
-                own = make_float4(A.x, X.x, A.y, X.y);
+    T *o = static_cast<T *>(p.o) + ((int64_t)u.tok0 + t0) * p.os + c;
+    const int stored = p.o ? u.mine : 0;
+    for (int step = 0, stage = 0; step < u.steps; ++step, t0 += cluster * kTile, o += (int64_t)cluster * kTile * p.os) {
+        const Span s = span_at<kSpan>(p, sh, u, t0, warp, lane, &seq);
+        copy_wait(stages - 1);
+        __syncwarp();
+        float2 a[kSpan], v[kSpan];
+        {
+            const T *x = reinterpret_cast<const T *>(mine + stage * kBytes);
+            const G *g = reinterpret_cast<const G *>(mine + stage * kBytes + kBytesX);
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i) {
+                const float2 gi = load2(g + i * kCh, lane);
+                a[i] = decay(gi);
+                v[i] = load2(x + i * kCh, lane);
+                if (COMP) v[i] = mul2(strength(gi, a[i]), v[i]);
             }
-        } else for (int k = 0; k < M; ++k) {
-            const Span s = span_at(p, sh, u, first + k * kSpan, warp, lane, &seq);
-            copy_wait(M - 1 - k);
-            __syncwarp();
-            float2 a[kSpan], v[kSpan];
-            load_span<COMP>(reinterpret_cast<const T *>(mine + k * kBytes), reinterpret_cast<const G *>(mine + k * kBytes + kBytesX), lane, a, v);
-            const float4 f = s.plain ? map_span<true>(p, u, a, v, 0, nullptr, c)
-                                     : map_span<false>(p, u, a, v, s.m.starts, start_of, c);
-            const float2 X = join(f, s.m.starts != 0, make_float2(own.y, own.w));
-            own = make_float4(own.x * f.x, X.x, own.z * f.z, X.y);
-            cuts |= s.m.starts != 0;
         }
+        __syncwarp();
+        fetch(stage);
+        if (++stage == stages) stage = 0;
+        float4 own;
+        if (s.plain) {
+            own = map_span<true>(p, u, a, v, 0, nullptr, c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i)
+                if (i >= s.count) a[i] = both(1.f), v[i] = both(0.f);
+            own = map_span<false>(p, u, a, v, s.m.starts, start_of, c);
+        }
+        const bool cuts = s.m.starts != 0;
         sh.spans[warp][lane] = own;
         if (lane == 0) sh.cut[warp] = cuts;
         const bool any = __syncthreads_or(cuts);
-        // the map of the warps before this one
+        // the map of the spans before this one
         float2 PA = both(1.f), PX = both(0.f);
         bool cut = false;
         if (!any) {
 #pragma unroll
             for (int j = 0; j < kWarps - 1; ++j)
                 if (j < warp) {
-                    const float4 s = sh.spans[j][lane];
-                    PX = fma2(make_float2(s.x, s.z), PX, make_float2(s.y, s.w));
-                    PA = mul2(PA, make_float2(s.x, s.z));
+                    const float4 f = sh.spans[j][lane];
+                    PX = fma2(make_float2(f.x, f.z), PX, make_float2(f.y, f.w));
+                    PA = mul2(PA, make_float2(f.x, f.z));
                 }
         } else {
 #pragma unroll 1
             for (int j = 0; j < warp; ++j) {
-                const float4 s = sh.spans[j][lane];
+                const float4 f = sh.spans[j][lane];
                 const bool here = sh.cut[j] & 1;
-                PX = join(s, here, PX);
-                PA = mul2(PA, make_float2(s.x, s.z));
+                PX = join(f, here, PX);
+                PA = mul2(PA, make_float2(f.x, f.z));
                 cut |= here;
             }
         }
@@ -619,31 +593,13 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
         }
         __syncthreads();
         if (sh.dead) break;
-        float2 h = cut ? PX : fma2(PA, sh.enter[lane], PX);
-        // second pass: the tokens, and the next step's in their place
-        seq = begin;
-        T *o = static_cast<T *>(p.o) + ((int64_t)u.tok0 + first) * p.os + c;
-        uint32_t save = p.states ? (first + p.saved_every - 1) / p.saved_every : 0;  // the next saved state
-        for (int k = 0; k < M; ++k, o += kSpan * p.os) {
-            const uint32_t t0 = first + k * kSpan;
-            if (p.states && t0 == save * p.saved_every) {
-                if (t0 < (uint32_t)u.S) store_state(p.states, (int64_t)(u.saved0 + save) * p.D + c, h, u.mine);
-                ++save;
-            }
-            Span s;
-            if (plain)
-                s.t0 = t0, s.count = kSpan, s.m = Marks{0, 0}, s.plain = true;
-            else
-                s = span_at(p, sh, u, t0, warp, lane, &seq);
-            float2 a[kSpan], v[kSpan];
-            load_span<COMP>(reinterpret_cast<const T *>(mine + k * kBytes), reinterpret_cast<const G *>(mine + k * kBytes + kBytesX), lane, a, v);
-            if (s.plain)
-                h = run_span<true, ALIGNED>(p, u, a, v, h, s, start_of, end_of, c, o);
-            else
-                h = run_span<false, ALIGNED>(p, u, a, v, h, s, start_of, end_of, c, o);
-            __syncwarp();
-            if (step + 1 < u.steps) fetch(first + cluster * u.tile + k * kSpan, k);
-        }
+        const float2 h = cut ? PX : fma2(PA, sh.enter[lane], PX);
+        if (p.states && t0 % kSaved == 0 && s.count)
+            store_state(p.states, (int64_t)(u.saved0 + t0 / kSaved) * p.D + c, h, u.mine);
+        if (s.plain)
+            run_span<true, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, o);
+        else
+            run_span<false, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, o);
     }
     copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
@@ -652,30 +608,28 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
 
 // ---------------------------------------------------------------- backward
 // The reverse map of a span; d: its tokens' gradients in shared memory.
-template <bool PLAIN, typename T>
+template <bool PLAIN, int kSpan, typename T>
 __device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan], const T *d,
-                                           int lane, uint32_t ends, const int *end_of, int c) {
+                                           int lane, const Span &s, const int *end_of, int c) {
     float2 Y = both(0.f);
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
-        if (!PLAIN && (ends >> i & 1)) Y = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
-        Y = mul2(a[i], add2(load2(d + i * kCh, lane), Y));
+        if (!PLAIN && (s.m.ends >> i & 1)) Y = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
+        if (PLAIN || i < s.count) Y = mul2(a[i], add2(load2(d + i * kCh, lane), Y));
     }
     return Y;
 }
 
 // The span's tokens: the states before them, then the gradients from the last to the first.
-template <bool PLAIN, bool COMP, bool EVEN, typename T, typename G>
-__device__ __forceinline__ float2 run_back(const LinrecParams &p, const Unit &u, const T *x, const T *d, const G *g,
-                                           int lane, float2 h, float2 r, const Span &s, const int *start_of,
-                                           const int *end_of, int c, T *dx, G *dg) {
-    float2 a[kSpan], w[kSpan], before[kSpan];
+template <bool PLAIN, bool COMP, bool EVEN, int kSpan, typename T, typename G>
+__device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
+                                         const float2 (&w)[kSpan], const T *x, const T *d, int lane, float2 h, float2 r,
+                                         const Span &s, const int *start_of, const int *end_of, int c, T *dx, G *dg) {
+    float2 before[kSpan];
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
-        const float2 gi = load2(g + i * kCh, lane), v = load2(x + i * kCh, lane);
-        a[i] = decay(gi);
-        w[i] = COMP ? strength(gi, a[i]) : both(1.f);
         if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        const float2 v = load2(x + i * kCh, lane);
         before[i] = COMP ? fma2(v, both(-1.f), h) : h;
         h = fma2(a[i], h, COMP ? mul2(w[i], v) : v);
     }
@@ -684,9 +638,9 @@ __device__ __forceinline__ float2 run_back(const LinrecParams &p, const Unit &u,
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
         if (!PLAIN && (s.m.ends >> i & 1)) r = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
-        const float2 e = add2(load2(d + i * kCh, lane), r);
-        r = mul2(a[i], e);
         if (PLAIN || i < s.count) {
+            const float2 e = add2(load2(d + i * kCh, lane), r);
+            r = mul2(a[i], e);
             store_pair<EVEN>(dx, COMP ? mul2(w[i], e) : e, u.mine);
             store_pair<EVEN>(dg, mul2(r, before[i]), u.mine);
         }
@@ -694,139 +648,141 @@ __device__ __forceinline__ float2 run_back(const LinrecParams &p, const Unit &u,
         dg -= p.dgs;
         if (!PLAIN && (s.m.starts >> i & 1)) store_state(p.dh0, start_of[i] * p.D + c, r, u.mine);
     }
-    return r;
 }
 
-template <typename T, typename G, bool COMP, bool ALIGNED>
+template <int kSpan, typename T, typename G, bool COMP, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Shared sh;
+    constexpr int kTile = kSpan * kWarps;
+    static_assert(kTile == kSaved, "a tile starts from a saved state");
     constexpr int kBytesX = kSpan * kCh * sizeof(T), kBytes = 2 * kBytesX + kSpan * kCh * sizeof(G);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, M = p.spans;
-    const Unit u = unit_of(p, lane);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = p.cluster, stages = p.stages;
+    const Unit u = unit_of(p, kTile, lane);
     const int c = u.c0 + 2 * lane;
-    unsigned char *mine = smem + warp * M * kBytes;
-    float4 *own_maps = reinterpret_cast<float4 *>(smem + kWarps * M * kBytes) + warp * M * 32 + lane;  // of the warp's spans
-    Map *maps = reinterpret_cast<Map *>(smem + kWarps * M * (kBytes + 32 * sizeof(float4)));
+    unsigned char *mine = smem + warp * stages * kBytes;
+    Map *maps = reinterpret_cast<Map *>(smem + kWarps * stages * kBytes);
     const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
     cluster_begin(sh, cluster);
 
-    const auto fetch = [&](uint32_t t0, int k) {
-        const int rows = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
-        const int64_t tok = (int64_t)u.tok0 + (rows ? t0 : 0);
-        T *x = reinterpret_cast<T *>(mine + k * kBytes), *d = reinterpret_cast<T *>(mine + k * kBytes + kBytesX);
-        G *g = reinterpret_cast<G *>(mine + k * kBytes + 2 * kBytesX);
-        copy_rows<ALIGNED>(x, static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
-        copy_rows<ALIGNED>(d, static_cast<const T *>(p.dy) + tok * p.os + u.c0, p.os, rows, u.cols, p.even, lane);
-        copy_rows<ALIGNED>(g, static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
+    // steps go from the stream's end
+    uint32_t t0 = ((uint32_t)(u.steps - 1) * cluster + u.rank) * kTile + warp * kSpan, ahead = t0;
+    int left = u.steps;  // steps whose copies are still to be made
+    const auto fetch = [&](int stage) {
+        const int rows = left <= 0 || ahead >= (uint32_t)u.S ? 0 : u.S - ahead < kSpan ? u.S - ahead : kSpan;
+        if (rows) {
+            const int64_t tok = (int64_t)u.tok0 + ahead;
+            unsigned char *to = mine + stage * kBytes;
+            copy_rows<kSpan, ALIGNED>(reinterpret_cast<T *>(to), static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
+            copy_rows<kSpan, ALIGNED>(reinterpret_cast<T *>(to + kBytesX), static_cast<const T *>(p.dy) + tok * p.os + u.c0, p.os, rows, u.cols, p.even, lane);
+            copy_rows<kSpan, ALIGNED>(reinterpret_cast<G *>(to + 2 * kBytesX), static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
+        }
         copy_commit();
+        ahead -= cluster * kTile;
+        --left;
     };
-    // steps go from the stream's end, spans from the warp's last
-    uint32_t tile = ((uint32_t)(u.steps - 1) * cluster + u.rank) * u.tile;
-    for (int k = M - 1; k >= 0; --k) fetch(tile + (warp * M + k) * kSpan, k);
+    // the state that enters a step's tile (the stream's first tile starts a sequence)
+    const auto saved = [&](uint32_t t) {
+        const uint32_t tile = t - warp * kSpan;
+        return tile > 0 && tile < (uint32_t)u.S ? load_state(p.states, (int64_t)(u.saved0 + tile / kSaved) * p.D + c, u.mine) : both(0.f);
+    };
+    for (int i = 0; i < stages; ++i) fetch(i);
     cluster_ready(cluster);
 
     Seq seq = {0, 0, 0};
     float2 carry = both(0.f);  // the gradient of the state that leaves the step (the first warp's)
-    for (int step = 0; step < u.steps; ++step, tile -= cluster * u.tile) {
-        const uint32_t first = tile + warp * M * kSpan;
-        // the state that enters the tile (the stream's first tile starts a sequence)
-        float2 h = both(0.f);
-        if (tile > 0 && tile < (uint32_t)u.S) h = load_state(p.states, (int64_t)(u.saved0 + tile / u.tile) * p.D + c, u.mine);
-        // first pass: the maps of the warp's tokens in both directions
-        const Seq begin = seq;
-        const bool plain = inside(p, u, seq, first, M * kSpan);
-        float2 A = both(1.f), X = both(0.f), Y = both(0.f);
-        bool starts = false, ends = false;
-        for (int k = M - 1; k >= 0; --k) {
-            Span s;
-            if (plain)
-                s.plain = true, s.m = Marks{0, 0};
-            else
-                s = span_at(p, sh, u, first + k * kSpan, warp, lane, &seq);
-            copy_wait(k);
-            __syncwarp();
-            const T *xs = reinterpret_cast<const T *>(mine + k * kBytes), *ds = reinterpret_cast<const T *>(mine + k * kBytes + kBytesX);
-            const G *gs = reinterpret_cast<const G *>(mine + k * kBytes + 2 * kBytesX);
-            float2 a[kSpan], v[kSpan], Yk;
-            load_span<COMP>(xs, gs, lane, a, v);
-            float4 f;
+    for (int step = 0, stage = 0; step < u.steps; ++step, t0 -= cluster * kTile) {
+        float2 h = saved(t0);
+        const Span s = span_at<kSpan>(p, sh, u, t0, warp, lane, &seq);
+        copy_wait(stages - 1);
+        __syncwarp();
+        const T *x = reinterpret_cast<const T *>(mine + stage * kBytes), *d = reinterpret_cast<const T *>(mine + stage * kBytes + kBytesX);
+        const G *g = reinterpret_cast<const G *>(mine + stage * kBytes + 2 * kBytesX);
+        // the span's maps in both directions
+        float2 a[kSpan], w[kSpan], Y;
+        float4 f;
+        {
+            float2 v[kSpan];
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i) {
+                const float2 gi = load2(g + i * kCh, lane);
+                a[i] = decay(gi);
+                w[i] = COMP ? strength(gi, a[i]) : both(1.f);
+                v[i] = load2(x + i * kCh, lane);
+                if (COMP) v[i] = mul2(w[i], v[i]);
+            }
             if (s.plain) {
                 f = map_span<true>(p, u, a, v, 0, nullptr, c);
-                Yk = map_back<true>(p, u, a, ds, lane, 0, end_of, c);
+                Y = map_back<true>(p, u, a, d, lane, s, end_of, c);
             } else {
+#pragma unroll
+                for (int i = 0; i < kSpan; ++i)
+                    if (i >= s.count) a[i] = both(1.f), v[i] = both(0.f);
                 f = map_span<false>(p, u, a, v, s.m.starts, start_of, c);
-                Yk = map_back<false>(p, u, a, ds, lane, s.m.ends, end_of, c);
+                Y = map_back<false>(p, u, a, d, lane, s, end_of, c);
             }
-            own_maps[k * 32] = f;
-            const float2 Ak = make_float2(f.x, f.z);
-            if (!starts) X = fma2(A, make_float2(f.y, f.w), X);
-            Y = s.m.ends ? Yk : fma2(Ak, Y, Yk);
-            A = mul2(A, Ak);
-            starts |= s.m.starts != 0;
-            ends |= s.m.ends != 0;
         }
-        const float4 own = make_float4(A.x, Y.x, A.y, Y.y);
+        const bool ends = s.m.ends != 0;
+        const float4 own = make_float4(f.x, Y.x, f.z, Y.y);
         sh.spans[warp][lane] = own;
-        sh.starts[warp][lane] = X;
-        if (lane == 0) sh.cut[warp] = starts | ends << 1;
-        __syncthreads();
-        // the reverse map of the warps after this one
+        sh.starts[warp][lane] = make_float2(f.y, f.w);
+        if (lane == 0) sh.cut[warp] = (s.m.starts != 0) | ends << 1;
+        const bool any = __syncthreads_or(s.m.starts | s.m.ends);
+        // the reverse map of the spans after this one, and the state that enters the span
         float2 PA = both(1.f), PY = both(0.f);
         bool cut = false;
+        if (!any) {
 #pragma unroll
-        for (int j = kWarps - 1; j > 0; --j)
-            if (j > warp) {
-                const float4 s = sh.spans[j][lane];
+            for (int j = kWarps - 1; j > 0; --j)
+                if (j > warp) {
+                    const float4 m = sh.spans[j][lane];
+                    PY = fma2(make_float2(m.x, m.z), PY, make_float2(m.y, m.w));
+                    PA = mul2(PA, make_float2(m.x, m.z));
+                }
+        } else {
+#pragma unroll 1
+            for (int j = kWarps - 1; j > warp; --j) {
+                const float4 m = sh.spans[j][lane];
                 const bool here = sh.cut[j] & 2;
-                PY = join(s, here, PY);
-                PA = mul2(PA, make_float2(s.x, s.z));
+                PY = join(m, here, PY);
+                PA = mul2(PA, make_float2(m.x, m.z));
                 cut |= here;
             }
+        }
+        float4 q;
         if (warp == 0) {
             const float2 R = join(own, ends, PY);
-            const float4 q = make_float4(PA.x * own.x, R.x, PA.y * own.z, R.y);
+            q = make_float4(PA.x * own.x, R.x, PA.y * own.z, R.y);
             send_map(p, sh, maps, u.rank, step, lane, q, cut || ends);
-            carry_on<true>(p, sh, maps, u.rank, step, lane, q, cut || ends, &carry);
         }
-        // the states that enter the warp's spans, in place of the spans' own
+        if (!any) {
 #pragma unroll
-        for (int j = 0; j < kWarps - 1; ++j)
-            if (j < warp) {
-                const float4 s = sh.spans[j][lane];
-                const float2 Xj = sh.starts[j][lane];
-                h = sh.cut[j] & 1 ? Xj : fma2(make_float2(s.x, s.z), h, Xj);
+            for (int j = 0; j < kWarps - 1; ++j)
+                if (j < warp) {
+                    const float4 m = sh.spans[j][lane];
+                    h = fma2(make_float2(m.x, m.z), h, sh.starts[j][lane]);
+                }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < warp; ++j) {
+                const float4 m = sh.spans[j][lane];
+                const float2 X = sh.starts[j][lane];
+                h = sh.cut[j] & 1 ? X : fma2(make_float2(m.x, m.z), h, X);
             }
-        seq = begin;
-        for (int k = 0; k < M - 1; ++k) {
-            const float4 f = own_maps[k * 32];
-            own_maps[k * 32] = make_float4(h.x, h.y, 0.f, 0.f);
-            // a start in the span: its X is the state that leaves it
-            h = !plain && span_at(p, sh, u, first + k * kSpan, warp, lane, &seq).m.starts ? make_float2(f.y, f.w) : fma2(make_float2(f.x, f.z), h, make_float2(f.y, f.w));
         }
-        own_maps[(M - 1) * 32] = make_float4(h.x, h.y, 0.f, 0.f);
+        if (warp == 0) carry_on<true>(p, sh, maps, u.rank, step, lane, q, cut || ends, &carry);
         __syncthreads();
         if (sh.dead) break;
-        float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
-        // second pass: the tokens, and the next step's in their place
-        for (int k = M - 1; k >= 0; --k) {
-            Span s;
-            if (plain)
-                s.t0 = first + k * kSpan, s.count = kSpan, s.m = Marks{0, 0}, s.plain = true;
-            else
-                s = span_at(p, sh, u, first + k * kSpan, warp, lane, &seq);
-            const T *xs = reinterpret_cast<const T *>(mine + k * kBytes), *ds = reinterpret_cast<const T *>(mine + k * kBytes + kBytesX);
-            const G *gs = reinterpret_cast<const G *>(mine + k * kBytes + 2 * kBytesX);
-            const float4 e = own_maps[k * 32];
-            T *dx = static_cast<T *>(p.dx) + ((int64_t)u.tok0 + s.t0) * p.dxs + c;
-            G *dg = static_cast<G *>(p.dg) + ((int64_t)u.tok0 + s.t0) * p.dgs + c;
-            if (s.plain)
-                r = run_back<true, COMP, ALIGNED>(p, u, xs, ds, gs, lane, make_float2(e.x, e.y), r, s, start_of, end_of, c, dx, dg);
-            else
-                r = run_back<false, COMP, ALIGNED>(p, u, xs, ds, gs, lane, make_float2(e.x, e.y), r, s, start_of, end_of, c, dx, dg);
-            __syncwarp();
-            if (step + 1 < u.steps) fetch(tile - cluster * u.tile + (warp * M + k) * kSpan, k);
-        }
+        const float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
+        T *dx = static_cast<T *>(p.dx) + ((int64_t)u.tok0 + t0) * p.dxs + c;
+        G *dg = static_cast<G *>(p.dg) + ((int64_t)u.tok0 + t0) * p.dgs + c;
+        if (s.plain)
+            run_back<true, COMP, ALIGNED>(p, u, a, w, x, d, lane, h, r, s, start_of, end_of, c, dx, dg);
+        else
+            run_back<false, COMP, ALIGNED>(p, u, a, w, x, d, lane, h, r, s, start_of, end_of, c, dx, dg);
+        __syncwarp();
+        fetch(stage);
+        if (++stage == stages) stage = 0;
     }
     copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
@@ -857,20 +813,51 @@ __global__ void __launch_bounds__(128) linrec_decode_kernel(LinrecParams p, floa
 // ---------------------------------------------------------------- launches
 enum class Pass { kFwd, kBwd, kDecode };
 
-// A kernel of `smem` bytes of dynamic shared memory on p's clusters.  The two attributes are set
-// once per device and kernel.
-cudaError_t launch_cluster(void (*kernel)(LinrecParams), std::atomic<uint64_t> *ready, const LinrecParams &p,
-                           size_t smem, cudaStream_t s) {
+using Kernel = void (*)(LinrecParams);
+
+// Clusters of each size (1 .. 16 CTAs, per_sm of them on an SM) that a device runs at once: they stay
+// within a group of SMs, so long ones fit less well (two CTAs per SM on a B200: 296 CTAs singly,
+// 264 in clusters of 8, 224 in clusters of 16).  Asked for once per kernel and device, with the
+// attributes that its launches need.
+struct Fit {
+    std::atomic<int32_t> known{0};
+    int16_t clusters[kMaxCluster + 1];
+};
+cudaError_t fit_of(Kernel kernel, int per_sm, Fit *fits, const Fit **out) {
+    constexpr int kDevices = 16;
+    static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (dev > 63 || !(ready->load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemSm - kSmemCta));
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        ready->fetch_or(bit, std::memory_order_relaxed);
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    Fit &fit = fits[dev];
+    *out = &fit;
+    if (fit.known.load(std::memory_order_acquire)) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(mu);
+    if (fit.known.load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemSm - kSmemCta));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int k = 1; k <= kMaxCluster && e == cudaSuccess; ++k) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = k;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(k);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemSm / per_sm - kSmemCta;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        fit.clusters[k] = (int16_t)n;
     }
+    if (e == cudaSuccess) fit.known.store(1, std::memory_order_release);
+    return e;
+}
+
+// A kernel of `smem` bytes of dynamic shared memory on p's clusters.
+cudaError_t launch_cluster(Kernel kernel, const LinrecParams &p, size_t smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.streams * p.slabs * p.cluster));
     cfg.blockDim = dim3(kThreads);
@@ -885,46 +872,32 @@ cudaError_t launch_cluster(void (*kernel)(LinrecParams), std::atomic<uint64_t> *
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// CTAs that run at once, two or three per SM, in clusters of 1, 2, 4, 8 and 16
-// (cudaOccupancyMaxActiveClusters on a B200: clusters stay within a group of SMs).
-int64_t capacity(int per_sm, int cluster) {
-    static const int kCtas[2][5] = {{296, 296, 284, 264, 224}, {444, 444, 416, 384, 336}};
-    int i = 0;
-    while (1 << i < cluster) ++i;
-    return kCtas[per_sm - 2][i];
-}
-
-// The cluster and the spans per warp for streams of p: the longest clusters that can all run at
-// once and that the stream fills; then as many spans as the stream gives its CTAs and their shared
-// memory holds.
-void plan(const LinrecParams &p, size_t span_bytes, int per_sm, int32_t *cluster, int32_t *spans) {
-    const int64_t rows = (p.rows_per_stream * p.T + kRows - 1) / kRows, units = p.streams * p.slabs;
-    int k = 1;
-    while (k < kMaxCluster && k < rows && units * k * 2 <= capacity(per_sm, k * 2)) k *= 2;
-    const size_t room = kSmemSm / per_sm - kSmemCta - (k > 1 ? 2 * k * sizeof(Map) : 0);
-    int64_t m = (int64_t)(room / (kWarps * span_bytes));
-    if (m > kMaxSpans) m = kMaxSpans;
-    if (m > (rows + k - 1) / k) m = (rows + k - 1) / k;
-    *cluster = k;
-    *spans = m < 1 ? 1 : (int32_t)m;
-}
-size_t fwd_span_bytes(int es, int ges) { return (size_t)kSpan * kCh * (es + ges); }
-size_t bwd_span_bytes(int es, int ges) { return (size_t)kSpan * kCh * (2 * es + ges) + 32 * sizeof(float4); }
-
 template <typename T, typename G, bool COMP, bool ALIGNED>
 cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
-    static std::atomic<uint64_t> ready[2];
+    static Fit fits[2][16];
     const bool fwd = pass == Pass::kFwd;
-    const size_t bytes = fwd ? fwd_span_bytes(sizeof(T), sizeof(G)) : bwd_span_bytes(sizeof(T), sizeof(G));
-    plan(p, bytes, fwd ? kFwdPerSm : kBwdPerSm, &p.cluster, &p.spans);
-    const size_t smem = kWarps * p.spans * bytes + (p.cluster > 1 ? 2 * p.cluster * sizeof(Map) : 0);
+    const int per_sm = fwd ? kFwdPerSm : kBwdPerSm, tile = kWarps * (fwd ? kFwdSpan<T> : kBwdSpan);
+    const size_t bytes = (size_t)tile * kCh * (fwd ? sizeof(T) + sizeof(G) : 2 * sizeof(T) + sizeof(G));
+    const int64_t tiles = (p.rows_per_stream * p.T + tile - 1) / tile, units = p.streams * p.slabs;
+    // the longest clusters that can all run at once, and that the stream fills
+    const Kernel kernel = fwd ? linrec_fwd_kernel<kFwdSpan<T>, T, G, COMP, ALIGNED> : linrec_bwd_kernel<kBwdSpan, T, G, COMP, ALIGNED>;
+    const Fit *fit = nullptr;
+    cudaError_t err = fit_of(kernel, per_sm, fits[fwd ? 0 : 1], &fit);
+    if (err != cudaSuccess) return err;
+    p.cluster = 1;
+    for (int k = 2; k <= kMaxCluster && k <= tiles; ++k)
+        if (units <= fit->clusters[k]) p.cluster = k;
+    // a ring of as many tiles as the shared memory holds, up to the steps there are
+    const int64_t steps = (tiles + p.cluster - 1) / p.cluster;
+    const size_t maps = p.cluster > 1 ? 2 * p.cluster * sizeof(Map) : 0;
+    int64_t stages = (int64_t)((kSmemSm / per_sm - kSmemCta - maps) / bytes);
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages > steps) stages = steps;
+    p.stages = stages < 1 ? 1 : (int32_t)stages;
+    const size_t smem = bytes * p.stages + maps;
     p.wait_limit = call_wait_limit();
     p.test_hook = call_test_hook();
-    cudaError_t err = cudaSuccess;
-    if (fwd)
-        GDN_LAUNCH(kKLinrecFwd, s, (err = launch_cluster(linrec_fwd_kernel<T, G, COMP, ALIGNED>, &ready[0], p, smem, s)));
-    else
-        GDN_LAUNCH(kKLinrecBwd, s, (err = launch_cluster(linrec_bwd_kernel<T, G, COMP, ALIGNED>, &ready[1], p, smem, s)));
+    GDN_LAUNCH(fwd ? kKLinrecFwd : kKLinrecBwd, s, (err = launch_cluster(kernel, p, smem, s)));
     return err;
 }
 
@@ -980,16 +953,12 @@ gdn_status describe(const gdn_linrec_desc *d, LinrecParams *p) {
     p->D = d->D;
     p->N = d->n_seqs > 0 ? d->n_seqs : d->B;
     // streams: the packed row, a dense row, or as many short dense rows as fill a tile
-    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kRows ? kRows / p->T : 1;
+    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kSaved ? kSaved / p->T : 1;
     p->streams = d->n_seqs > 0 ? 1 : (p->N + p->rows_per_stream - 1) / p->rows_per_stream;
     p->single = d->n_seqs > 0 ? d->n_seqs == 1 : p->rows_per_stream == 1;
     p->slabs = (int32_t)((p->D + kCh - 1) / kCh);
     if (p->streams * p->slabs >= kLim / kMaxCluster) return GDN_ERR_INVALID_ARG;
-    // a saved state for every tile of the backward
-    int32_t cluster, spans;
-    plan(*p, bwd_span_bytes(d->dtype == GDN_BF16 ? 2 : 4, d->g_dtype == GDN_BF16 ? 2 : 4), kBwdPerSm, &cluster, &spans);
-    p->saved_every = kRows * spans;
-    p->saved = (p->rows_per_stream * p->T + p->saved_every - 1) / p->saved_every;
+    p->saved = (p->rows_per_stream * p->T + kSaved - 1) / kSaved;
     const int64_t in[] = {d->x_stride, d->g_stride, d->o_stride, d->dx_stride, d->dg_stride};
     int64_t *out[] = {&p->xs, &p->gs, &p->os, &p->dxs, &p->dgs};
     for (int i = 0; i < 5; ++i) {
