@@ -1,5 +1,16 @@
 // Normalisation of q and k per token and head with the position rotation, and its
-// gradients (declared in include/gdn.h): one warp per row, the row in shared memory.
+// gradients (declared in include/gdn.h).
+//
+// A row (one token and head) is split into units of two 16-byte chunks that turn into
+// each other: the values i .. i + V and their partners i + rot / 2 .., or two adjacent chunks
+// where pairs are adjacent or nothing turns.  A lane holds one unit, so norm and rotation
+// need no exchange but the sum of squares over the row's lanes (8 lanes of a bf16 row of
+// 128), and 32 / lanes heads of a token run side by side in a warp.  A warp walks the heads
+// of its tokens with a ring of loads kUnroll rows deep; the angles of a token are formed
+// once per warp (64-bit product and reduction, sincospi of the fraction) and shared through
+// shared memory by all its heads.  Bound by HBM: every row is read and written once.  The
+// weights' gradients are summed in registers over a block's rows, written once per block, and
+// added in block order by a second kernel.
 #include <cmath>
 
 #include "gdn_internal.cuh"
@@ -7,11 +18,16 @@
 namespace gdn {
 namespace {
 
-constexpr int kMaxD = 256, kWarps = 8, kSlots = 592;
+constexpr int kMaxD = 256, kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kSms = 148, kPerSm = 3;            // blocks of an SM
+constexpr int kSlots = kSms * kPerSm;           // blocks at most, of both tensors
 
 struct QkParams {
     int64_t tokens;
     int32_t T, d, rot, norm, interleaved;
+    int32_t lanes, lanes_log2;  // lanes of a row
+    int32_t blocks[2];          // blocks of q and of k
+    int32_t per[2], parts[2];   // rows (times 32 / lanes) of a warp's item, and items of a token
     float c, eps;
     const int32_t *pos;
     const float *inv_freq;
@@ -24,127 +40,377 @@ struct QkParams {
     float *dw[2], *part;
 };
 
-__device__ __forceinline__ float ld(const float *p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float ld(const __nv_bfloat16 *p, int64_t i) {
-    return __bfloat162float(p[i]);
-}
-__device__ __forceinline__ void st(float *p, int64_t i, float x) { p[i] = x; }
-__device__ __forceinline__ void st(__nv_bfloat16 *p, int64_t i, float x) {
-    p[i] = __float2bfloat16_rn(x);
-}
-
-__device__ __forceinline__ float total(float s) {
+// ---------------------------------------------------------------- small pieces
+// V values of a row: as loaded, and in fp32.  VEC: one load of V values, else one by one.
+template <typename T, int V, bool VEC>
+struct Chunk;
+template <int V, bool VEC>
+struct Chunk<float, V, VEC> {
+    float r[V];
+    __device__ __forceinline__ void load(const float *p) {
+        if (VEC && V == 4) {
+            const float4 t = __ldcs(reinterpret_cast<const float4 *>(p));
+            r[0] = t.x, r[1 % V] = t.y, r[2 % V] = t.z, r[3 % V] = t.w;
+        } else {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    return s;
-}
+            for (int i = 0; i < V; ++i) r[i] = p[i];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = 0.f;
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = r[i];
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[V]) {
+        if (VEC && V == 4) {
+            *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1 % V], x[2 % V], x[3 % V]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = x[i];
+        }
+    }
+};
+template <int V, bool VEC>
+struct Chunk<__nv_bfloat16, V, VEC> {
+    static constexpr int kWords = (V + 1) / 2;
+    uint32_t r[kWords];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        if (VEC && V == 8) {
+            const uint4 t = __ldcs(reinterpret_cast<const uint4 *>(p));
+            r[0] = t.x, r[1 % kWords] = t.y, r[2 % kWords] = t.z, r[3 % kWords] = t.w;
+        } else if (VEC && V == 4) {
+            const uint2 t = __ldcs(reinterpret_cast<const uint2 *>(p));
+            r[0] = t.x, r[1 % kWords] = t.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                r[i / 2] = __bfloat16_as_ushort(p[i]);
+                if (i + 1 < V) r[i / 2] |= (uint32_t)__bfloat16_as_ushort(p[i + 1]) << 16;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) r[i] = 0;
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[V]) {
+        if (VEC) {
+            uint32_t t[kWords];
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[(i + 1) % V]);
+                t[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            if (V == 8)
+                *reinterpret_cast<uint4 *>(p) = make_uint4(t[0], t[1 % kWords], t[2 % kWords], t[3 % kWords]);
+            else
+                *reinterpret_cast<uint2 *>(p) = make_uint2(t[0], t[1 % kWords]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = __float2bfloat16_rn(x[i]);
+        }
+    }
+};
 
-// cos and sin of pos * freq: the angle in turns in 64 bits, its fraction in 32.
-__device__ __forceinline__ void turn(int32_t pos, float freq, float *c, float *s) {
-    const double t = (double)pos * (double)freq * 0.15915494309189533577;
-    sincospif(2.f * (float)(t - rint(t)), s, c);
-}
-
-// Value i of the row: its pair's other value, its angle's index (-1: not turned) and the
-// sign of sin at the other value.
-__device__ __forceinline__ void partner(const QkParams &p, int i, int *j, int *f, float *sign) {
-    const int half = p.rot / 2;
-    *f = -1, *j = i, *sign = 0.f;
-    if (i >= p.rot) return;
-    const bool first = p.interleaved ? !(i & 1) : i < half;
-    *j = p.interleaved ? i ^ 1 : first ? i + half : i - half;
-    *f = p.interleaved ? i / 2 : first ? i : i - half;
-    *sign = first ? -1.f : 1.f;
-}
-
+// 1 / sqrt(c |x|^2 + eps), 0 for 0.
 __device__ __forceinline__ float scale_of(const QkParams &p, float sum) {
     if (p.norm == GDN_NORM_NONE) return 1.f;
     const float m = fmaf(p.c, sum, p.eps);
-    return m > 0.f ? 1.f / sqrtf(m) : m == 0.f ? 0.f : m;
+    return m > 0.f ? rsqrtf(m) : m;
 }
 
-template <typename T, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps) qk_kernel(QkParams p) {
-    __shared__ float rows[kWarps][kMaxD], sums[kWarps][kMaxD];
-    const int l = threadIdx.x & 31, wi = threadIdx.x >> 5, which = blockIdx.y;
-    const int64_t n = p.tokens * p.heads[which];
+// A pair of chunks turned by the angles whose (cos, sin) are given (BACK: turned back).  Adjacent
+// pairs: the first V / 2 angles are the first chunk's.
+template <int V, bool ADJ, bool BACK>
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *angles) {
+    float2 cs[V];
+    if (V % 2 == 0) {  // two angles per load
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float4 t = *reinterpret_cast<const float4 *>(angles + e);
+            cs[e] = make_float2(t.x, t.y), cs[(e + 1) % V] = make_float2(t.z, t.w);
+        }
+    } else {
+        cs[0] = angles[0];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float c = cs[e].x, sn = BACK ? -cs[e].y : cs[e].y;
+        if (!ADJ) {
+            const float u = a[e], v = b[e];
+            a[e] = fmaf(u, c, -v * sn);
+            b[e] = fmaf(u, sn, v * c);
+        } else {
+            float(&t)[V] = e < V / 2 ? a : b;
+            const int i = 2 * (e % (V / 2 ? V / 2 : 1));
+            const float u = t[i], v = t[(i + 1) % V];
+            t[i] = fmaf(u, c, -v * sn);
+            t[(i + 1) % V] = fmaf(u, sn, v * c);
+        }
+    }
+}
+
+// A warp's way through its rows: items (a token's heads, or a part of them) and the rows of an item.
+struct Way {
+    uint32_t item, tok;
+    int it, end;
+};
+
+// ---------------------------------------------------------------- the kernel
+// NU units per lane.  VEC: whole chunks are loaded and stored at once.
+template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD>
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
+    constexpr int kUnroll = NU > 1 ? 1 : BWD ? 2 : 2;
+    __shared__ __align__(16) float2 angles[kWarps][kMaxD / 2 + 8];  // (cos, sin); (1, 0) behind the turned values
+    __shared__ float sums[BWD ? kWarps : 1][kMaxD];
+    const int l = threadIdx.x & 31, wi = threadIdx.x >> 5;
+    const int which = blockIdx.x >= p.blocks[0], block = blockIdx.x - (which ? p.blocks[0] : 0);
+    const int H = p.heads[which], half = p.rot / 2, d = p.d;
+    const int side = 32 >> p.lanes_log2, sub = l >> p.lanes_log2, unit = l & (p.lanes - 1);
     const T *x = static_cast<const T *>(p.x[which]), *dy = static_cast<const T *>(p.dy[which]);
     T *out = static_cast<T *>(BWD ? p.dx[which] : p.y[which]);
-    const int64_t os = BWD ? p.dxs[which] : p.ys[which];
-    const float *w = p.w[which];
-    float *row = rows[wi], acc[kMaxD / 32] = {};
-    for (int64_t r = (int64_t)blockIdx.x * kWarps + wi; r < n; r += (int64_t)gridDim.x * kWarps) {
-        const int64_t tok = r / p.heads[which];
-        const int h = (int)(r % p.heads[which]);
-        const int32_t pos = p.pos ? p.pos[tok] : (int32_t)(tok % p.T);
-        const T *xr = x + tok * p.xs[which] + (int64_t)h * p.d;
-        float s = 0.f;
-        for (int i = l; i < p.d; i += 32) s = fmaf(ld(xr, i), ld(xr, i), s);
-        const float inv = scale_of(p, total(s));
-        for (int i = l; i < p.d; i += 32)
-            row[i] = BWD ? ld(dy, tok * p.ys[which] + (int64_t)h * p.d + i)
-                         : ld(xr, i) * inv * (w ? w[i] : 1.f);
-        __syncwarp();
-        T *o = out + tok * os + (int64_t)h * p.d;
-        float u[kMaxD / 32], dot = 0.f;
-        for (int i = l, m = 0; i < p.d; i += 32, ++m) {
-            int j, f;
-            float sign, c = 1.f, sn = 0.f;
-            partner(p, i, &j, &f, &sign);
-            if (f >= 0) turn(pos, p.inv_freq[f], &c, &sn);
-            if (BWD) {
-                u[m] = fmaf(row[j], -sign * sn, row[i] * c);
-                const float xn = ld(xr, i) * inv;
-                acc[m] = fmaf(u[m], xn, acc[m]);
-                u[m] *= w ? w[i] : 1.f;
-                dot = fmaf(u[m], xn, dot);
-            } else {
-                st(o, i, fmaf(row[j], sign * sn, row[i] * c));
+    const int64_t xs = p.xs[which], ys = p.ys[which], os = BWD ? p.dxs[which] : ys;
+    const int its = (H + side - 1) / side, per = p.per[which], parts = p.parts[which];
+    const uint32_t items = (uint32_t)p.tokens * parts, warps = p.blocks[which] * kWarps;
+
+    // this lane's units: where their chunks are (-1: nowhere) and their first angle
+    int at[NU][2], angle[NU];
+    float w[NU][2][V], acc[NU][2][V];
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+        const int j = unit + k * p.lanes;
+        if (ADJ || j * V < half) {
+            at[k][0] = ADJ ? 2 * j * V : j * V;
+            at[k][1] = at[k][0] + (ADJ ? V : half);
+            angle[k] = j * V;
+        } else {  // behind the turned values
+            at[k][0] = p.rot + 2 * (j * V - half);
+            at[k][1] = at[k][0] + V;
+            angle[k] = kMaxD / 2;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (at[k][e] >= d) at[k][e] = -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                w[k][e][i] = p.w[which] && at[k][e] >= 0 ? p.w[which][at[k][e] + i] : 1.f;
+                acc[k][e][i] = 0.f;
             }
         }
-        if (BWD) {
-            dot = p.norm == GDN_NORM_NONE ? 0.f : p.c * total(dot);
-            for (int i = l, m = 0; i < p.d; i += 32, ++m)
-                st(o, i, inv * fmaf(-(ld(xr, i) * inv), dot, u[m]));
+    }
+    for (int i = half + l; i < kMaxD / 2 + 8; i += 32) angles[wi][i] = make_float2(1.f, 0.f);
+
+    const auto enter = [&](Way &y) {
+        y.tok = y.item / parts;
+        y.it = (y.item - y.tok * parts) * per;
+        y.end = y.it + per < its ? y.it + per : its;
+    };
+    const auto advance = [&](Way &y) {
+        if (++y.it < y.end) return;
+        y.item += warps;
+        if (y.item < items) enter(y);
+    };
+    Chunk<T, V, VEC> rx[kUnroll][NU][2], rd[BWD ? kUnroll : 1][NU][2];
+    int32_t pos[kUnroll];
+    const auto load = [&](const Way &y, int u) {
+        const int h = y.it * side + sub;
+        const bool in = y.item < items && h < H;
+        const T *px = x + y.tok * xs + (int64_t)h * d, *pd = BWD ? dy + y.tok * ys + (int64_t)h * d : nullptr;
+        if (y.item < items) pos[u] = p.pos ? p.pos[y.tok] : (int32_t)(y.tok % (uint32_t)p.T);
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool here = in && at[k][e] >= 0;
+                rx[u][k][e].zero();
+                if (here) rx[u][k][e].load(px + at[k][e]);
+                if (BWD) {
+                    rd[u][k][e].zero();
+                    if (here) rd[u][k][e].load(pd + at[k][e]);
+                }
+            }
+    };
+
+    Way go = {(uint32_t)(block * kWarps + wi), 0, 0, 0}, ahead = go;
+    if (go.item < items) enter(go);
+    ahead = go;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        load(ahead, u);
+        if (ahead.item < items) advance(ahead);
+    }
+    uint32_t angles_of = ~0u;  // token whose angles are at hand
+    while (go.item < items) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (go.item >= items) break;
+            if (angles_of != go.tok) {
+                angles_of = go.tok;
+                __syncwarp();
+                for (int i = l; i < half; i += 32) {
+                    const double t = (double)pos[u] * ((double)p.inv_freq[i] * 0.15915494309189533577);
+                    float2 cs;
+                    sincospif(2.f * (float)(t - rint(t)), &cs.y, &cs.x);
+                    angles[wi][i] = cs;
+                }
+                __syncwarp();
+            }
+            float a[NU][2][V], g[NU][2][V], s = 0.f, dot = 0.f;
+#pragma unroll
+            for (int k = 0; k < NU; ++k) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    rx[u][k][e].get(a[k][e]);
+                    if (BWD) rd[u][k][e].get(g[k][e]);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s = fmaf(a[k][e][i], a[k][e][i], s);
+                }
+                if (BWD) {
+                    turn<V, ADJ, true>(g[k][0], g[k][1], angles[wi] + angle[k]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) dot = fmaf(g[k][e][i] * w[k][e][i], a[k][e][i], dot);
+                }
+            }
+            for (int off = p.lanes >> 1; off > 0; off >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, off);
+                if (BWD) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            }
+            const float r = scale_of(p, s);
+            const float cd = p.norm == GDN_NORM_NONE ? 0.f : p.c * (r * dot);
+            const int h = go.it * side + sub;
+            T *o = out + go.tok * os + (int64_t)h * d;
+#pragma unroll
+            for (int k = 0; k < NU; ++k) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float xn = a[k][e][i] * r;
+                        if (BWD) {
+                            acc[k][e][i] = fmaf(g[k][e][i], xn, acc[k][e][i]);
+                            a[k][e][i] = r * fmaf(-xn, cd, g[k][e][i] * w[k][e][i]);
+                        } else {
+                            a[k][e][i] = xn * w[k][e][i];
+                        }
+                    }
+                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], angles[wi] + angle[k]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (h < H && at[k][e] >= 0) Chunk<T, V, VEC>::store(o + at[k][e], a[k][e]);
+            }
+            load(ahead, u);
+            if (ahead.item < items) advance(ahead);
+            advance(go);
         }
-        __syncwarp();
     }
     if (BWD && p.dw[which]) {
-        for (int i = l, m = 0; i < p.d; i += 32, ++m) sums[wi][i] = acc[m];
+        // over the heads side by side, then over the block's warps
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float t = acc[k][e][i];
+                    for (int off = 16; off >= p.lanes; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+                    if (sub == 0 && at[k][e] >= 0) sums[wi][at[k][e] + i] = t;
+                }
         __syncthreads();
-        for (int i = threadIdx.x; i < p.d; i += 32 * kWarps) {
-            float s = 0.f;
-            for (int k = 0; k < kWarps; ++k) s += sums[k][i];
-            p.part[((int64_t)which * kSlots + blockIdx.x) * kMaxD + i] = s;
+        for (int i = threadIdx.x; i < d; i += kThreads) {
+            float t = 0.f;
+            for (int k = 0; k < kWarps; ++k) t += sums[k][i];
+            p.part[(int64_t)blockIdx.x * kMaxD + i] = t;
         }
     }
 }
 
-__global__ void __launch_bounds__(kMaxD) qk_dw_kernel(QkParams p, int blocks) {
-    const int i = threadIdx.x, which = blockIdx.x;
-    if (i >= p.d || !p.dw[which]) return;
+// The weights' gradients from the blocks' sums: 32 values per block of 32 x 32 threads.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const __grid_constant__ QkParams p) {
+    __shared__ float sums[32][33];
+    const int which = blockIdx.y, i = blockIdx.x * 32 + threadIdx.x;
+    if (!p.dw[which]) return;
+    const float *part = p.part + (which ? (int64_t)p.blocks[0] * kMaxD : 0);
     float s = 0.f;
-    for (int b = 0; b < blocks; ++b) s += p.part[((int64_t)which * kSlots + b) * kMaxD + i];
-    p.dw[which][i] = s;
+    if (i < p.d)
+        for (int b = threadIdx.y; b < p.blocks[which]; b += 32) s += part[(int64_t)b * kMaxD + i];
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && i < p.d) {
+        s = 0.f;
+        for (int b = 0; b < 32; ++b) s += sums[b][threadIdx.x];
+        p.dw[which][i] = s;
+    }
+}
+
+// ---------------------------------------------------------------- launches
+template <typename T, int V, int NU, bool VEC, bool ADJ>
+cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
+    // lanes of a row: a power of two that its units fit
+    const int half = p.rot / 2, units = ADJ ? (p.d + 2 * V - 1) / (2 * V) : half / V + (p.d - p.rot + 2 * V - 1) / (2 * V);
+    p.lanes_log2 = 0;
+    while ((1 << p.lanes_log2) < (units + NU - 1) / NU) ++p.lanes_log2;
+    p.lanes = 1 << p.lanes_log2;
+    const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? 2 : kPerSm);
+    // a warp takes all heads of a token, or fewer where that leaves warps without work
+    int64_t rows[2], blocks[2];
+    for (int i = 0; i < 2; ++i) rows[i] = (p.heads[i] + side - 1) / side;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t fair = p.tokens * (rows[0] + rows[1]) / (most * kWarps);  // rows per warp if all had some
+        p.per[i] = (int32_t)(fair < 1 ? 1 : fair < rows[i] ? fair : rows[i]);
+        p.parts[i] = (int32_t)((rows[i] + p.per[i] - 1) / p.per[i]);
+        blocks[i] = (p.tokens * p.parts[i] + kWarps - 1) / kWarps;
+        if (blocks[i] < 1) blocks[i] = 1;
+    }
+    if (blocks[0] + blocks[1] > most) {  // share them out by the work, and walk
+        int64_t q = most * rows[0] / (rows[0] + rows[1]);
+        q = q < 1 ? 1 : q > most - 1 ? most - 1 : q;
+        if (q < blocks[0]) blocks[0] = q;
+        if (most - q < blocks[1]) blocks[1] = most - q;
+    }
+    p.blocks[0] = (int32_t)blocks[0];
+    p.blocks[1] = (int32_t)blocks[1];
+    const unsigned grid = (unsigned)(blocks[0] + blocks[1]);
+    if (!bwd) {
+        if (p.tokens) GDN_LAUNCH(kKQkRope, s, qk_kernel<T, V, NU, VEC, ADJ, false><<<grid, kThreads, 0, s>>>(p));
+        return cudaSuccess;
+    }
+    if (p.tokens || p.dw[0] || p.dw[1])
+        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, V, NU, VEC, ADJ, true><<<grid, kThreads, 0, s>>>(p));
+    if (p.dw[0] || p.dw[1])
+        GDN_LAUNCH(kKQkRopeDw, s, qk_dw_kernel<<<dim3((p.d + 31) / 32, 2), dim3(32, 32), 0, s>>>(p));
+    return cudaSuccess;
+}
+
+// Whether rows split into whole, aligned chunks of v values.
+bool chunks(const QkParams &p, bool bwd, int v) {
+    int64_t all = p.d | p.xs[0] | p.xs[1] | p.ys[0] | p.ys[1];
+    if (bwd) all |= p.dxs[0] | p.dxs[1];
+    if (!p.interleaved) all |= p.rot / 2;
+    return all % v == 0;
 }
 
 template <typename T>
 cudaError_t launch(const QkParams &p, bool bwd, cudaStream_t s) {
-    const int64_t most = p.tokens * (p.heads[0] > p.heads[1] ? p.heads[0] : p.heads[1]);
-    const int64_t want = (most + kWarps - 1) / kWarps;
-    const dim3 grid((unsigned)(want < 1 ? 1 : want < kSlots ? want : kSlots), 2);
-    if (!bwd) {
-        if (p.tokens) GDN_LAUNCH(kKQkRope, s, qk_kernel<T, false><<<grid, 32 * kWarps, 0, s>>>(p));
-        return cudaSuccess;
-    }
-    if (p.tokens || p.dw[0] || p.dw[1])
-        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, true><<<grid, 32 * kWarps, 0, s>>>(p));
-    if (p.dw[0] || p.dw[1])
-        GDN_LAUNCH(kKQkRopeDw, s, qk_dw_kernel<<<2, kMaxD, 0, s>>>(p, (int)grid.x));
-    return cudaSuccess;
+    // 16-byte chunks; bf16 rows whose halves or strides are multiples of 4 only: 8-byte ones; other
+    // rows value by value
+    constexpr int kWide = 16 / sizeof(T);
+    if (chunks(p, bwd, kWide))
+        return p.interleaved ? launch_units<T, kWide, 1, true, true>(p, bwd, s) : launch_units<T, kWide, 1, true, false>(p, bwd, s);
+    if (sizeof(T) == 2 && chunks(p, bwd, 4))
+        return p.interleaved ? launch_units<T, 4, 1, true, true>(p, bwd, s) : launch_units<T, 4, 1, true, false>(p, bwd, s);
+    return p.interleaved ? launch_units<T, 2, 4, false, true>(p, bwd, s) : launch_units<T, 1, 4, false, false>(p, bwd, s);
 }
 
-size_t workspace_bytes_needed() { return sizeof(float) * 2 * kSlots * kMaxD; }
+size_t workspace_bytes_needed() { return sizeof(float) * kSlots * kMaxD; }
 
 // Checks that need no pointers; fills the sizes and strides.
 gdn_status describe(const gdn_qk_desc *d, QkParams *p) {
