@@ -19,13 +19,14 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxD = 256, kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSms = 148, kPerSm = 3;            // blocks of an SM
+constexpr int kSms = 148, kPerSm = 3, kBwdPerSm = 2;            // blocks of an SM
 constexpr int kSlots = kSms * kPerSm;           // blocks at most, of both tensors
 
 struct QkParams {
     int64_t tokens;
     int32_t T, d, rot, norm, interleaved;
     int32_t lanes, lanes_log2;  // lanes of a row
+    int32_t whole;              // every lane has both chunks of its units
     int32_t blocks[2];          // blocks of q and of k
     int32_t per[2], parts[2];   // rows (times 32 / lanes) of a warp's item, and items of a token
     float c, eps;
@@ -126,15 +127,42 @@ __device__ __forceinline__ float scale_of(const QkParams &p, float sum) {
     return m > 0.f ? rsqrtf(m) : m;
 }
 
+// Where value i of chunk e of unit j is among the weights in shared memory: fours of neighbouring
+// units side by side, so that a row's lanes read adjacent 16 bytes.
+template <int V>
+__device__ __forceinline__ int weight_at(int n, int j, int e, int i) {
+    return V % 4 ? (e * V + i) * n + j : ((e * (V / 4) + i / 4) * n + j) * 4 + i % 4;
+}
+template <int V>
+__device__ __forceinline__ void weights_of(const float *from, int n, int j, int e, float (&w)[V]) {
+    if (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(from + weight_at<V>(n, j, e, i));
+            w[i] = t.x, w[(i + 1) % V] = t.y, w[(i + 2) % V] = t.z, w[(i + 3) % V] = t.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = from[weight_at<V>(n, j, e, i)];
+    }
+}
+
+// Where angle i of unit j is among a warp's: pairs of angles of neighbouring units side by side, so
+// that a row's lanes read adjacent 16 bytes.  n: units and one for what is not turned.
+template <int V>
+__device__ __forceinline__ int angle_at(int n, int j, int i) {
+    return V % 2 ? n * i + j : 2 * (n * (i / 2) + j) + i % 2;
+}
+
 // A pair of chunks turned by the angles whose (cos, sin) are given (BACK: turned back).  Adjacent
 // pairs: the first V / 2 angles are the first chunk's.
 template <int V, bool ADJ, bool BACK>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *angles) {
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *angles, int n) {
     float2 cs[V];
     if (V % 2 == 0) {  // two angles per load
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-            const float4 t = *reinterpret_cast<const float4 *>(angles + e);
+            const float4 t = *reinterpret_cast<const float4 *>(angles + angle_at<V>(n, 0, e));
             cs[e] = make_float2(t.x, t.y), cs[(e + 1) % V] = make_float2(t.z, t.w);
         }
     } else {
@@ -158,18 +186,23 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 
 }
 
 // A warp's way through its rows: items (a token's heads, or a part of them) and the rows of an item.
+// row, drow: where this lane's row is, for reading (x, dy) or writing.
+template <typename P>
 struct Way {
     uint32_t item, tok;
     int it, end;
+    int32_t pos;
+    P row, drow;
 };
 
 // ---------------------------------------------------------------- the kernel
 // NU units per lane.  VEC: whole chunks are loaded and stored at once.
 template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? 2 : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
-    constexpr int kUnroll = NU > 1 ? 1 : BWD ? 2 : 2;
-    __shared__ __align__(16) float2 angles[kWarps][kMaxD / 2 + 8];  // (cos, sin); (1, 0) behind the turned values
+__global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
+    constexpr int kUnroll = NU > 1 ? 1 : BWD ? 1 : 2;
+    __shared__ __align__(16) float2 angles[kWarps][kMaxD / 2 + 8];  // (cos, sin), see angle_at
     __shared__ float sums[BWD ? kWarps : 1][kMaxD];
+    __shared__ __align__(16) float weights[kMaxD];
     const int l = threadIdx.x & 31, wi = threadIdx.x >> 5;
     const int which = blockIdx.x >= p.blocks[0], block = blockIdx.x - (which ? p.blocks[0] : 0);
     const int H = p.heads[which], half = p.rot / 2, d = p.d;
@@ -180,72 +213,89 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : kPerSm) qk_kernel(const __
     const int its = (H + side - 1) / side, per = p.per[which], parts = p.parts[which];
     const uint32_t items = (uint32_t)p.tokens * parts, warps = p.blocks[which] * kWarps;
 
-    // this lane's units: where their chunks are (-1: nowhere) and their first angle
+    const int units = NU * p.lanes + 1;
+    // this lane's units: where their chunks are (-1: nowhere) and whose angles they take
     int at[NU][2], angle[NU];
-    float w[NU][2][V], acc[NU][2][V];
+    float acc[NU][2][V];
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
         const int j = unit + k * p.lanes;
         if (ADJ || j * V < half) {
             at[k][0] = ADJ ? 2 * j * V : j * V;
             at[k][1] = at[k][0] + (ADJ ? V : half);
-            angle[k] = j * V;
+            angle[k] = j;
         } else {  // behind the turned values
             at[k][0] = p.rot + 2 * (j * V - half);
             at[k][1] = at[k][0] + V;
-            angle[k] = kMaxD / 2;
+            angle[k] = units - 1;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (at[k][e] >= d) at[k][e] = -1;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                w[k][e][i] = p.w[which] && at[k][e] >= 0 ? p.w[which][at[k][e] + i] : 1.f;
                 acc[k][e][i] = 0.f;
+                if (wi == 0 && sub == 0)
+                    weights[weight_at<V>(units - 1, j, e, i)] = p.w[which] && at[k][e] >= 0 ? p.w[which][at[k][e] + i] : 1.f;
             }
         }
     }
-    for (int i = half + l; i < kMaxD / 2 + 8; i += 32) angles[wi][i] = make_float2(1.f, 0.f);
+    for (int i = half + l; i < units * V; i += 32) angles[wi][angle_at<V>(units, i / V, i % V)] = make_float2(1.f, 0.f);
 
-    const auto enter = [&](Way &y) {
+    __syncthreads();
+    // whole: every lane has both chunks of its units, and every row of lanes a head
+    const bool whole = VEC && NU == 1 && H % side == 0 && p.whole;
+    const int64_t step = (int64_t)side * d;
+    const auto enter = [&](auto &y, auto base, int64_t stride) {
         y.tok = y.item / parts;
         y.it = (y.item - y.tok * parts) * per;
         y.end = y.it + per < its ? y.it + per : its;
-    };
-    const auto advance = [&](Way &y) {
-        if (++y.it < y.end) return;
-        y.item += warps;
-        if (y.item < items) enter(y);
+        y.row = base + y.tok * stride + (int64_t)(y.it * side + sub) * d;
     };
     Chunk<T, V, VEC> rx[kUnroll][NU][2], rd[BWD ? kUnroll : 1][NU][2];
     int32_t pos[kUnroll];
-    const auto load = [&](const Way &y, int u) {
-        const int h = y.it * side + sub;
-        const bool in = y.item < items && h < H;
-        const T *px = x + y.tok * xs + (int64_t)h * d, *pd = BWD ? dy + y.tok * ys + (int64_t)h * d : nullptr;
-        if (y.item < items) pos[u] = p.pos ? p.pos[y.tok] : (int32_t)(y.tok % (uint32_t)p.T);
+    Way<const T *> ahead = {(uint32_t)(block * kWarps + wi), 0, 0, 0, 0, nullptr, nullptr};
+    Way<T *> go = {ahead.item, 0, 0, 0, 0, nullptr, nullptr};
+    const auto enter_ahead = [&]() {
+        if (ahead.item >= items) return;
+        enter(ahead, x, xs);
+        if (BWD) ahead.drow = dy + ahead.tok * ys + (int64_t)(ahead.it * side + sub) * d;
+        ahead.pos = p.pos ? p.pos[ahead.tok] : (int32_t)(ahead.tok % (uint32_t)p.T);
+    };
+    // loads the row that `ahead` is at, and moves on
+    const auto load = [&](int u) {
+        if (ahead.item >= items) return;
+        pos[u] = ahead.pos;
+        const bool in = whole || ahead.it * side + sub < H;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool here = in && at[k][e] >= 0;
-                rx[u][k][e].zero();
-                if (here) rx[u][k][e].load(px + at[k][e]);
-                if (BWD) {
-                    rd[u][k][e].zero();
-                    if (here) rd[u][k][e].load(pd + at[k][e]);
+                if (whole) {
+                    rx[u][k][e].load(ahead.row + at[k][e]);
+                    if (BWD) rd[u][k][e].load(ahead.drow + at[k][e]);
+                } else {
+                    const bool here = in && at[k][e] >= 0;
+                    rx[u][k][e].zero();
+                    if (here) rx[u][k][e].load(ahead.row + at[k][e]);
+                    if (BWD) {
+                        rd[u][k][e].zero();
+                        if (here) rd[u][k][e].load(ahead.drow + at[k][e]);
+                    }
                 }
             }
+        ahead.row += step;
+        if (BWD) ahead.drow += step;
+        if (++ahead.it == ahead.end) {
+            ahead.item += warps;
+            enter_ahead();
+        }
     };
 
-    Way go = {(uint32_t)(block * kWarps + wi), 0, 0, 0}, ahead = go;
-    if (go.item < items) enter(go);
-    ahead = go;
+    enter_ahead();
+    if (go.item < items) enter(go, out, os);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        load(ahead, u);
-        if (ahead.item < items) advance(ahead);
-    }
+    for (int u = 0; u < kUnroll; ++u) load(u);
     uint32_t angles_of = ~0u;  // token whose angles are at hand
     while (go.item < items) {
 #pragma unroll
@@ -258,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : kPerSm) qk_kernel(const __
                     const double t = (double)pos[u] * ((double)p.inv_freq[i] * 0.15915494309189533577);
                     float2 cs;
                     sincospif(2.f * (float)(t - rint(t)), &cs.y, &cs.x);
-                    angles[wi][i] = cs;
+                    angles[wi][angle_at<V>(units, i / V, i % V)] = cs;
                 }
                 __syncwarp();
             }
@@ -273,11 +323,14 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : kPerSm) qk_kernel(const __
                     for (int i = 0; i < V; ++i) s = fmaf(a[k][e][i], a[k][e][i], s);
                 }
                 if (BWD) {
-                    turn<V, ADJ, true>(g[k][0], g[k][1], angles[wi] + angle[k]);
+                    turn<V, ADJ, true>(g[k][0], g[k][1], angles[wi] + angle_at<V>(units, angle[k], 0), units);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e) {
+                        float w[V];
+                        weights_of<V>(weights, units - 1, unit + k * p.lanes, e, w);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dot = fmaf(g[k][e][i] * w[k][e][i], a[k][e][i], dot);
+                        for (int i = 0; i < V; ++i) dot = fmaf(g[k][e][i] * w[i], a[k][e][i], dot);
+                    }
                 }
             }
             for (int off = p.lanes >> 1; off > 0; off >>= 1) {
@@ -286,30 +339,35 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : kPerSm) qk_kernel(const __
             }
             const float r = scale_of(p, s);
             const float cd = p.norm == GDN_NORM_NONE ? 0.f : p.c * (r * dot);
-            const int h = go.it * side + sub;
-            T *o = out + go.tok * os + (int64_t)h * d;
+            const bool in = whole || go.it * side + sub < H;
 #pragma unroll
             for (int k = 0; k < NU; ++k) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e) {
+                    float w[V];
+                    weights_of<V>(weights, units - 1, unit + k * p.lanes, e, w);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float xn = a[k][e][i] * r;
                         if (BWD) {
                             acc[k][e][i] = fmaf(g[k][e][i], xn, acc[k][e][i]);
-                            a[k][e][i] = r * fmaf(-xn, cd, g[k][e][i] * w[k][e][i]);
+                            a[k][e][i] = r * fmaf(-xn, cd, g[k][e][i] * w[i]);
                         } else {
-                            a[k][e][i] = xn * w[k][e][i];
+                            a[k][e][i] = xn * w[i];
                         }
                     }
-                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], angles[wi] + angle[k]);
+                }
+                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], angles[wi] + angle_at<V>(units, angle[k], 0), units);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (h < H && at[k][e] >= 0) Chunk<T, V, VEC>::store(o + at[k][e], a[k][e]);
+                    if (whole || (in && at[k][e] >= 0)) Chunk<T, V, VEC>::store(go.row + at[k][e], a[k][e]);
             }
-            load(ahead, u);
-            if (ahead.item < items) advance(ahead);
-            advance(go);
+            load(u);
+            go.row += step;
+            if (++go.it == go.end) {
+                go.item += warps;
+                if (go.item < items) enter(go, out, os);
+            }
         }
     }
     if (BWD && p.dw[which]) {
@@ -359,7 +417,8 @@ cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
     p.lanes_log2 = 0;
     while ((1 << p.lanes_log2) < (units + NU - 1) / NU) ++p.lanes_log2;
     p.lanes = 1 << p.lanes_log2;
-    const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? 2 : kPerSm);
+    p.whole = NU == 1 && p.lanes * 2 * V == p.d;
+    const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? kBwdPerSm : kPerSm);
     // a warp takes all heads of a token, or fewer where that leaves warps without work
     int64_t rows[2], blocks[2];
     for (int i = 0; i < 2; ++i) rows[i] = (p.heads[i] + side - 1) / side;
