@@ -68,6 +68,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libgdn.so (raises if it was not built: there is no other path)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -282,6 +284,8 @@ def gdn_decode(q, k, v, g, beta, state, scale=1.0, o=None, stream=None, qk_l2nor
 
 # ------------------------------------------------------- gated linear recurrence
 _DT = {torch.bfloat16: GDN_BF16, torch.float32: GDN_FP32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 class _Here:
@@ -297,44 +301,51 @@ class _Here:
 _here = _Here()
 
 
-def _scope(device, stream, used):
-    """(context, stream) of a call whose tensors live on ``device``: allocations and
-    launches go to ``stream`` (None: that device's current stream), whatever the current
-    device is; tensors used on another stream than the current one are recorded on it."""
-    if device.type != "cuda":
+def _scope(first, stream, used):
+    """(context, device index, stream handle) of a call whose tensors live on the first one's
+    device: allocations and launches go to ``stream`` (None: that device's current stream),
+    whatever the current device is; tensors used on another stream than the current one are
+    recorded on it."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    cur = torch.cuda.current_stream(device)
-    if stream is None or stream == cur:
-        if torch.cuda.current_device() == device.index:
-            return _here, cur
-        return torch.cuda.stream(cur), cur
-    if stream.device != device:
-        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
-    for t in used:
-        if t is not None and t.is_cuda:
-            t.record_stream(stream)
-    return torch.cuda.stream(stream), stream
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return _here, index, _raw_stream(index)
+        stream = torch.cuda.current_stream(index)
+    elif stream.device.index != index:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, first.device))
+    elif stream != torch.cuda.current_stream(index):
+        for t in used:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+    return torch.cuda.stream(stream), index, stream.cuda_stream
 
 
-def _check_on(t, name, device, dtype=None, shape=None):
-    """_check, and that t lives on the call's device."""
-    _check(t, name, dtype, shape)
-    if t is not None and t.device != device:
-        raise ValueError("%s is on %s, the call's tensors on %s" % (name, t.device, device))
+def _like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
-def _row_stride(t, name, device, dtype, shape):
+def _pointer(t, name, index, dtype, shape):
+    """Address of a contiguous tensor of this type and shape (None: any) on the call's device;
+    None for None."""
+    if t is None:
+        return None
+    if (t.get_device() != index or t.dtype is not dtype or not t.is_contiguous() or
+            (shape is not None and t.shape != shape)):
+        _check(t, name, dtype, shape)
+        raise ValueError("%s is on %s, the call's tensors on cuda:%d" % (name, t.device, index))
+    return t.data_ptr()
+
+
+def _row_stride(t, name, dtype, shape):
     """Elements from one token to the next of a (B, T, ...) tensor whose values of one token
     are adjacent and whose tokens are evenly spaced over all rows (a column slice of a wider
     contiguous tensor is; a transposed or expanded one is not)."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, the call's tensors on %s" % (name, t.device, device))
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.is_contiguous():
         return 0
     width = 1
@@ -349,19 +360,72 @@ def _row_stride(t, name, device, dtype, shape):
     return s
 
 
-def _linrec_desc(x, g, n_seqs, complement, do=None, o=None, dx=None, dg=None):
+def _rows(t, name, index):
+    """What a descriptor depends on of a tensor of rows, after the check of its device."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        raise ValueError("%s is on %s, the call's tensors on cuda:%d" % (name, t.device, index))
+    return t.dtype, t.shape, t.stride()
+
+
+class _Plans(dict):
+    """Descriptors of earlier calls by what they are made of (types, shapes, strides, options)."""
+    limit = 1024
+
+    def keep(self, key, plan):
+        if len(self) >= self.limit:
+            self.clear()
+        self[key] = plan
+        return plan
+
+
+_linrec_plans, _qk_plans = _Plans(), _Plans()
+
+
+def _linrec_plan(x, g, index, n_seqs, complement, do=None, o=None, dx=None, dg=None):
+    """(descriptor, reference to it, bytes of states)."""
+    key = (_rows(x, "x", index), _rows(g, "g", index), n_seqs, bool(complement),
+           _rows(do, "do", index), _rows(o, "o", index), _rows(dx, "dx", index),
+           _rows(dg, "dg", index))
+    plan = _linrec_plans.get(key)
+    if plan is not None:
+        return plan
     if x.dim() != 3:
         raise ValueError("x must have shape (B, T, D), got %s" % (tuple(x.shape),))
     if x.dtype not in _DT:
         raise ValueError("x must be bf16 or fp32")
     if g.dtype not in (x.dtype, torch.float32):
         raise ValueError("g must be %s or torch.float32, got %s" % (x.dtype, g.dtype))
-    shape, dev = tuple(x.shape), x.device
-    row = lambda t, name, dt: 0 if t is None else _row_stride(t, name, dev, dt, shape)
-    return GdnLinrecDesc(*shape, n_seqs, row(x, "x", x.dtype), row(g, "g", g.dtype),
+    shape = tuple(x.shape)
+    row = lambda t, name, dt: 0 if t is None else _row_stride(t, name, dt, shape)
+    desc = GdnLinrecDesc(*shape, n_seqs, row(x, "x", x.dtype), row(g, "g", g.dtype),
                          row(do, "do", x.dtype) if do is not None else row(o, "o", x.dtype),
                          row(dx, "dx", x.dtype), row(dg, "dg", g.dtype), _DT[x.dtype],
                          _DT[g.dtype], GDN_LINREC_COMPLEMENT if complement else 0, 0)
+    ref = ctypes.byref(desc)
+    return _linrec_plans.keep(key, (desc, ref, int(lib().gdn_linrec_states_size(ref))))
+
+
+def _offsets(cu_seqlens, cu_seqlens_host, index):
+    """(device offsets, their address, the host mirror's address, number of documents)."""
+    if cu_seqlens is None and cu_seqlens_host is None:
+        return None, None, None, 0
+    if (cu_seqlens is None or cu_seqlens_host is None or cu_seqlens.get_device() != index or
+            cu_seqlens.dtype is not torch.int32 or cu_seqlens_host.dtype is not torch.int32 or
+            not cu_seqlens.is_contiguous() or not cu_seqlens_host.is_contiguous()):
+        if cu_seqlens is not None and cu_seqlens.is_cuda and cu_seqlens.get_device() != index:
+            raise ValueError("cu_seqlens is on %s, the call's tensors on cuda:%d"
+                             % (cu_seqlens.device, index))
+        cu_seqlens, cu_seqlens_host = _seqlens(cu_seqlens, cu_seqlens_host,
+                                               torch.device("cuda", index))
+    if cu_seqlens.shape != cu_seqlens_host.shape or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must have one dimension and 2 values or more, and its host "
+                         "mirror the same number")
+    return (cu_seqlens, cu_seqlens_host), cu_seqlens.data_ptr(), cu_seqlens_host.data_ptr(), \
+        cu_seqlens_host.numel() - 1
 
 
 def gdn_linrec_fwd(x, g, cu_seqlens=None, h0=None, complement=False, output_final_state=True,
@@ -372,32 +436,26 @@ def gdn_linrec_fwd(x, g, cu_seqlens=None, h0=None, complement=False, output_fina
     slices of a wider tensor; h0: (N, D) fp32.  Returns (o, hT), or (o, hT, states) with
     ``save_states``: a buffer that spares gdn_linrec_bwd recomputing the states."""
     L = lib()
-    dev = x.device
-    scope, stream = _scope(dev, stream, (x, g, h0, cu_seqlens, o, hT, states))
+    scope, index, handle = _scope(x, stream, (x, g, h0, cu_seqlens, o, hT, states))
     with scope:
-        cu_dev, cu_host = _seqlens(cu_seqlens, cu_seqlens_host, dev)
-        n_seqs = 0 if cu_host is None else cu_host.numel() - 1
-        desc = _linrec_desc(x, g, n_seqs, complement, o=o)
+        _kept, cu, cu_host, n_seqs = _offsets(cu_seqlens, cu_seqlens_host, index)
+        _, ref, need = _linrec_plan(x, g, index, n_seqs, complement, o=o)
         N = (n_seqs or x.shape[0], x.shape[2])
-        _check_on(h0, "h0", dev, torch.float32, N)
-        _check_on(hT, "hT", dev, torch.float32, N)
-        _check_on(cu_dev, "cu_seqlens", dev)
-        _check_on(states, "states", dev, torch.uint8)
         if o is None:
-            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            o = _like(x)
         if hT is None and output_final_state:
-            hT = torch.empty(N, dtype=torch.float32, device=dev)
+            hT = x.new_empty(N, dtype=torch.float32)
         if save_states or states is not None:
-            need = L.gdn_linrec_states_size(ctypes.byref(desc))
             if need == 0:
                 raise GdnError(1, "gdn_linrec_states_size")
             if states is None:
-                states = torch.empty(need, dtype=torch.uint8, device=dev)
+                states = x.new_empty(need, dtype=torch.uint8)
             elif states.numel() < need:
                 raise GdnError(4, "gdn_linrec_fwd")
-        rc = L.gdn_linrec_fwd(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), _ptr(cu_dev),
-                              _ptr(cu_host), _ptr(h0), o.data_ptr(), _ptr(hT), _ptr(states),
-                              stream.cuda_stream)
+        rc = L.gdn_linrec_fwd(ref, x.data_ptr(), g.data_ptr(), cu, cu_host,
+                              _pointer(h0, "h0", index, torch.float32, N), o.data_ptr(),
+                              _pointer(hT, "hT", index, torch.float32, N),
+                              _pointer(states, "states", index, torch.uint8, None), handle)
     if rc:
         raise GdnError(rc, "gdn_linrec_fwd")
     return (o, hT, states) if states is not None else (o, hT)
@@ -409,36 +467,31 @@ def gdn_linrec_bwd(x, g, do, cu_seqlens=None, h0=None, dhT=None, complement=Fals
     ABI.  ``states``: what gdn_linrec_fwd returned for the same x, g, cu_seqlens and h0; without
     it the states are recomputed into the workspace."""
     L = lib()
-    dev = x.device
     dx, dg, dh0 = grads if grads is not None else (None, None, None)
-    scope, stream = _scope(dev, stream, (x, g, do, h0, dhT, cu_seqlens, dx, dg, dh0, states,
-                                         workspace))
+    scope, index, handle = _scope(x, stream, (x, g, do, h0, dhT, cu_seqlens, dx, dg, dh0, states,
+                                              workspace))
     with scope:
-        cu_dev, cu_host = _seqlens(cu_seqlens, cu_seqlens_host, dev)
-        n_seqs = 0 if cu_host is None else cu_host.numel() - 1
-        desc = _linrec_desc(x, g, n_seqs, complement, do=do, dx=dx, dg=dg)
+        _kept, cu, cu_host, n_seqs = _offsets(cu_seqlens, cu_seqlens_host, index)
+        _, ref, need = _linrec_plan(x, g, index, n_seqs, complement, do=do, dx=dx, dg=dg)
         N = (n_seqs or x.shape[0], x.shape[2])
-        for t, name in ((h0, "h0"), (dhT, "dhT"), (dh0, "dh0")):
-            _check_on(t, name, dev, torch.float32, N)
-        _check_on(cu_dev, "cu_seqlens", dev)
-        _check_on(states, "states", dev, torch.uint8)
-        _check_on(workspace, "workspace", dev, torch.uint8)
         if grads is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
-            dh0 = torch.empty(N, dtype=torch.float32, device=dev) if want_dh0 else None
-        need = L.gdn_linrec_states_size(ctypes.byref(desc))
+            dx = _like(x)
+            dg = _like(g)
+            dh0 = x.new_empty(N, dtype=torch.float32) if want_dh0 else None
         if need == 0:
             raise GdnError(1, "gdn_linrec_states_size")
         if states is not None:
             if states.numel() < need:
                 raise GdnError(4, "gdn_linrec_bwd")
         elif workspace is None:
-            workspace = alloc_workspace(need, dev)
-        rc = L.gdn_linrec_bwd(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), _ptr(cu_dev),
-                              _ptr(cu_host), _ptr(h0), do.data_ptr(), _ptr(dhT), _ptr(dx),
-                              _ptr(dg), _ptr(dh0), _ptr(states), _ptr(workspace),
-                              0 if workspace is None else workspace.numel(), stream.cuda_stream)
+            workspace = x.new_empty(need, dtype=torch.uint8)
+        rc = L.gdn_linrec_bwd(ref, x.data_ptr(), g.data_ptr(), cu, cu_host,
+                              _pointer(h0, "h0", index, torch.float32, N), do.data_ptr(),
+                              _pointer(dhT, "dhT", index, torch.float32, N), _ptr(dx), _ptr(dg),
+                              _pointer(dh0, "dh0", index, torch.float32, N),
+                              _pointer(states, "states", index, torch.uint8, None),
+                              _pointer(workspace, "workspace", index, torch.uint8, None),
+                              0 if workspace is None else workspace.numel(), handle)
     if rc:
         raise GdnError(rc, "gdn_linrec_bwd")
     return dx, dg, dh0
@@ -453,16 +506,14 @@ def linrec_status(stream=None) -> int:
 def gdn_linrec_decode(x, g, state, complement=False, o=None, stream=None):
     """One-token form through the C ABI: advances ``state`` ((B, D) fp32, in place) through the
     T tokens of x and g ((B, T, D)) and returns o."""
-    L = lib()
-    dev = x.device
-    scope, stream = _scope(dev, stream, (x, g, state, o))
+    scope, index, handle = _scope(x, stream, (x, g, state, o))
     with scope:
-        desc = _linrec_desc(x, g, 0, complement, o=o)
-        _check_on(state, "state", dev, torch.float32, (x.shape[0], x.shape[2]))
+        _, ref, _ = _linrec_plan(x, g, index, 0, complement, o=o)
         if o is None:
-            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        rc = L.gdn_linrec_decode(ctypes.byref(desc), x.data_ptr(), g.data_ptr(), state.data_ptr(),
-                                 o.data_ptr(), stream.cuda_stream)
+            o = _like(x)
+        rc = lib().gdn_linrec_decode(ref, x.data_ptr(), g.data_ptr(),
+                                     _pointer(state, "state", index, torch.float32,
+                                              (x.shape[0], x.shape[2])), o.data_ptr(), handle)
     if rc:
         raise GdnError(rc, "gdn_linrec_decode")
     return o
@@ -472,31 +523,44 @@ def gdn_linrec_decode(x, g, state, complement=False, o=None, stream=None):
 _NORMS = {None: (GDN_NORM_NONE, 0.0), "l2": (GDN_NORM_L2, 0.0), "rms": (GDN_NORM_RMS, 1e-6)}
 
 
-def _qk_call(q, k, inv_freq, positions, norm, q_weight, k_weight, eps, interleaved, outs, raws):
-    """Checks of the arguments both passes share, and the descriptor.  outs: the rotated q and k
-    or their gradients, raws: the gradients of the raw q and k (None where not given)."""
+def _qk_plan(q, k, inv_freq, norm, eps, interleaved, index, outs, raws):
+    """(descriptor, reference to it, bytes of the backward's workspace).  outs: the rotated q and
+    k or their gradients, raws: the gradients of the raw q and k (None where not given)."""
+    turned = 0 if inv_freq is None else inv_freq.numel()
+    key = (_rows(q, "q", index), _rows(k, "k", index), turned, norm, eps, bool(interleaved),
+           _rows(outs[0], "qo", index), _rows(outs[1], "ko", index), _rows(raws[0], "dq", index),
+           _rows(raws[1], "dk", index))
+    plan = _qk_plans.get(key)
+    if plan is not None:
+        return plan
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must have shape (B, T, heads, d)")
     if q.dtype not in _DT:
         raise ValueError("q must be bf16 or fp32")
     if norm not in _NORMS:
         raise ValueError("norm must be None, 'l2' or 'rms', got %r" % (norm,))
-    dev = q.device
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
     B, T, Hq, d = q.shape
     Hk = k.shape[2]
     shapes = ((B, T, Hq, d), (B, T, Hk, d))
-    row = lambda t, name, i: 0 if t is None else _row_stride(t, name, dev, q.dtype, shapes[i])
-    _check_on(inv_freq, "inv_freq", dev, torch.float32)
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must have one dimension")
-    _check_on(positions, "positions", dev, torch.int32, (B, T))
-    _check_on(q_weight, "q_weight", dev, torch.float32, (d,))
-    _check_on(k_weight, "k_weight", dev, torch.float32, (d,))
+    row = lambda t, name, i: 0 if t is None else _row_stride(t, name, q.dtype, shapes[i])
     code, default = _NORMS[norm]
-    return GdnQkDesc(B, T, Hq, Hk, d, 0 if inv_freq is None else 2 * inv_freq.numel(),
-                     row(q, "q", 0), row(k, "k", 1), row(outs[0], "qo", 0), row(outs[1], "ko", 1),
-                     row(raws[0], "dq", 0), row(raws[1], "dk", 1), _DT[q.dtype], code,
+    desc = GdnQkDesc(B, T, Hq, Hk, d, 2 * turned, row(q, "q", 0), row(k, "k", 1),
+                     row(outs[0], "qo", 0), row(outs[1], "ko", 1), row(raws[0], "dq", 0),
+                     row(raws[1], "dk", 1), _DT[q.dtype], code,
                      GDN_QK_INTERLEAVED if interleaved else 0, default if eps is None else eps)
+    ref = ctypes.byref(desc)
+    return _qk_plans.keep(key, (desc, ref, int(lib().gdn_qk_norm_rope_bwd_workspace_size(ref))))
+
+
+def _qk_inputs(q, positions, inv_freq, q_weight, k_weight, index):
+    """Addresses of the inputs beside the rows."""
+    d = q.shape[3:]
+    return (_pointer(positions, "positions", index, torch.int32, q.shape[:2]),
+            _pointer(inv_freq, "inv_freq", index, torch.float32, None),
+            _pointer(q_weight, "q_weight", index, torch.float32, d),
+            _pointer(k_weight, "k_weight", index, torch.float32, d))
 
 
 def gdn_qk_norm_rope_fwd(q, k, inv_freq=None, positions=None, norm="rms", q_weight=None,
@@ -505,22 +569,18 @@ def gdn_qk_norm_rope_fwd(q, k, inv_freq=None, positions=None, norm="rms", q_weig
     """Rows of q (B, T, Hq, d) and k (B, T, Hk, d) normalised (``norm``: "rms", "l2" or None),
     multiplied by the weights (d,) fp32, and turned by the angles positions x inv_freq
     (positions: (B, T) int32, or None to count along each row; inv_freq: (rot/2,) fp32, or None
-    for no rotation), through the C ABI.  eps defaults to 1e-6 for "rms" and 0 for "l2".
-    Returns (qo, ko)."""
-    L = lib()
-    dev = q.device
-    scope, stream = _scope(dev, stream, (q, k, inv_freq, positions, q_weight, k_weight, qo, ko))
+    for no rotation), through the C ABI.  q and k may be column slices of one projection.  eps
+    defaults to 1e-6 for "rms" and 0 for "l2".  Returns (qo, ko)."""
+    scope, index, handle = _scope(q, stream, (q, k, inv_freq, positions, q_weight, k_weight, qo, ko))
     with scope:
-        desc = _qk_call(q, k, inv_freq, positions, norm, q_weight, k_weight, eps, interleaved,
-                        (qo, ko), (None, None))
+        _, ref, _ = _qk_plan(q, k, inv_freq, norm, eps, interleaved, index, (qo, ko), (None, None))
         if qo is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            qo = _like(q)
         if ko is None:
-            ko = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        rc = L.gdn_qk_norm_rope_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(),
-                                    _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
-                                    _ptr(k_weight), qo.data_ptr(), ko.data_ptr(),
-                                    stream.cuda_stream)
+            ko = _like(k)
+        rc = lib().gdn_qk_norm_rope_fwd(ref, q.data_ptr(), k.data_ptr(),
+                                        *_qk_inputs(q, positions, inv_freq, q_weight, k_weight, index),
+                                        qo.data_ptr(), ko.data_ptr(), handle)
     if rc:
         raise GdnError(rc, "gdn_qk_norm_rope_fwd")
     return qo, ko
@@ -531,34 +591,26 @@ def gdn_qk_norm_rope_bwd(q, k, dqo, dko, inv_freq=None, positions=None, norm="rm
                          workspace=None, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of gdn_qk_norm_rope_fwd for upstream dqo, dko,
     through the C ABI; a weight that is None has no gradient (None)."""
-    L = lib()
-    dev = q.device
     dq, dk, dqw, dkw = grads if grads is not None else (None, None, None, None)
-    scope, stream = _scope(dev, stream, (q, k, dqo, dko, inv_freq, positions, q_weight, k_weight,
-                                         dq, dk, dqw, dkw, workspace))
+    scope, index, handle = _scope(q, stream, (q, k, dqo, dko, inv_freq, positions, q_weight,
+                                              k_weight, dq, dk, dqw, dkw, workspace))
     with scope:
-        desc = _qk_call(q, k, inv_freq, positions, norm, q_weight, k_weight, eps, interleaved,
-                        (dqo, dko), (dq, dk))
-        d = (q.shape[3],)
-        _check_on(dqw, "dq_weight", dev, torch.float32, d)
-        _check_on(dkw, "dk_weight", dev, torch.float32, d)
-        _check_on(workspace, "workspace", dev, torch.uint8)
+        _, ref, need = _qk_plan(q, k, inv_freq, norm, eps, interleaved, index, (dqo, dko), (dq, dk))
+        d = q.shape[3:]
         if grads is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-            dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-            dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-        if workspace is None and (dqw is not None or dkw is not None):
-            need = L.gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(desc))
-            if need == 0:
-                raise GdnError(2, "gdn_qk_norm_rope_bwd_workspace_size")
-            workspace = alloc_workspace(need, dev)
-        rc = L.gdn_qk_norm_rope_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(),
-                                    _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
-                                    _ptr(k_weight), dqo.data_ptr(), dko.data_ptr(), _ptr(dq),
-                                    _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace),
-                                    0 if workspace is None else workspace.numel(),
-                                    stream.cuda_stream)
+            dq = _like(q)
+            dk = _like(k)
+            dqw = None if q_weight is None else q.new_empty(d, dtype=torch.float32)
+            dkw = None if k_weight is None else q.new_empty(d, dtype=torch.float32)
+        if workspace is None and need and (dqw is not None or dkw is not None):
+            workspace = q.new_empty(need, dtype=torch.uint8)
+        rc = lib().gdn_qk_norm_rope_bwd(ref, q.data_ptr(), k.data_ptr(),
+                                        *_qk_inputs(q, positions, inv_freq, q_weight, k_weight, index),
+                                        dqo.data_ptr(), dko.data_ptr(), _ptr(dq), _ptr(dk),
+                                        _pointer(dqw, "dq_weight", index, torch.float32, d),
+                                        _pointer(dkw, "dk_weight", index, torch.float32, d),
+                                        _pointer(workspace, "workspace", index, torch.uint8, None),
+                                        0 if workspace is None else workspace.numel(), handle)
     if rc:
         raise GdnError(rc, "gdn_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw

@@ -123,10 +123,8 @@ def test_binding_refuses_before_any_call():
 
 
 def test_head_strides():
-    from test_linrec_host import OnGpu
-
     from gated_delta_rule_99_b200._binding import _row_stride
-    stride = lambda t: _row_stride(OnGpu(t), "q", OnGpu.device, torch.float32, tuple(t.shape))
+    stride = lambda t: _row_stride(t, "q", torch.float32, tuple(t.shape))
     wide = torch.zeros(2, 5, 40)
     assert stride(wide[..., 8:24].unflatten(-1, (2, 8))) == 40
     for bad in (wide.unflatten(-1, (5, 8))[:, :, ::2], wide.unflatten(-1, (5, 8))[..., :4],
