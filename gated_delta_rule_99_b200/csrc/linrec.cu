@@ -50,6 +50,9 @@ struct LinrecParams {
     int64_t streams, rows_per_stream;  // a stream: one dense row, several short ones, or the packed row
     int64_t saved;                            // saved states of a stream
     int32_t slabs, cluster, stages, aligned, even;
+    // bytes from a token to the next, and from a step of the cluster to the next
+    int64_t x_row, g_row, dy_row, o_row, dx_row, dg_row;
+    int64_t x_step, g_step, dy_step, o_step, dx_step, dg_step;
     uint32_t wait_limit;
     int32_t test_hook;
     int32_t single;  // every stream is one sequence
@@ -168,9 +171,28 @@ __device__ __forceinline__ void copy_wait(int pending) {
     }
 }
 
+// The copies of whole spans whose rows start on 16 bytes: a lane copies 16 bytes (the last ones maybe
+// in part, the rest become zeros) of every kAtOnce-th row, from a pointer that moves with the steps.
+template <int kSpan, typename E>
+struct Copies {
+    static constexpr int kPer = 16 / sizeof(E), kPieces = kCh / kPer, kAtOnce = 32 / kPieces;
+    const char *src;  // the lane's piece of the span's first rows
+    int bytes, at;    // how much of it exists, and where it goes in a span
+    __device__ __forceinline__ void start(const void *base, int64_t tok, int64_t row, const int c0, int cols, int lane) {
+        const int c = lane % kPieces * kPer, r = lane / kPieces, here = (cols - c) * (int)sizeof(E);
+        bytes = here < 0 ? 0 : here > 16 ? 16 : here;
+        at = r * kCh + c;
+        src = static_cast<const char *>(base) + (tok + r) * row + (c0 + (bytes ? c : 0)) * (int64_t)sizeof(E);
+    }
+    __device__ __forceinline__ void span(E *dst, int64_t row) const {
+#pragma unroll
+        for (int i = 0; i < kSpan; i += kAtOnce) copy_async16(dst + at + i * kCh, src + i * row, bytes);
+    }
+};
+
 // A span's tokens x 64 channels; `rows` and `cols` of them exist, the rest become zeros.  Rows that
-// start on 16 bytes: 16 at a time (the last ones maybe in part); fp32, or bf16 with even rows: 4 at
-// a time; else one bf16 after another.
+// start on 16 bytes: 16 at a time; fp32, or bf16 with even rows: 4 at a time; else one bf16 after
+// another.
 template <int kSpan, bool ALIGNED, typename E>
 __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, int rows, int cols,
                                           int even, int lane) {
@@ -179,16 +201,10 @@ __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, 
         const int c = lane % kPieces * kPer, r = lane / kPieces;
         const int here = (cols - c) * (int)sizeof(E), bytes = here < 0 ? 0 : here > 16 ? 16 : here;
         dst += r * kCh + c;
-        if (rows == kSpan) {
-            src += bytes ? r * stride + c : 0;
 #pragma unroll
-            for (int i = 0; i < kSpan; i += kAtOnce) copy_async16(dst + i * kCh, src + i * stride, bytes);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kSpan; i += kAtOnce) {
-                const int n = i + r < rows ? bytes : 0;
-                copy_async16(dst + i * kCh, n ? src + (i + r) * stride + c : src, n);
-            }
+        for (int i = 0; i < kSpan; i += kAtOnce) {
+            const int n = i + r < rows ? bytes : 0;
+            copy_async16(dst + i * kCh, n ? src + (i + r) * stride + c : src, n);
         }
     } else if (sizeof(E) == 4 || even) {
         constexpr int kPer = 4 / sizeof(E);
@@ -512,7 +528,7 @@ __device__ __forceinline__ void run_span(const LinrecParams &p, const Unit &u, c
         if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
         h = fma2(a[i], h, v[i]);
         if (PLAIN || i < s.count) store_pair<EVEN>(o, h, mine);
-        o += p.os;
+        o = reinterpret_cast<T *>(reinterpret_cast<char *>(o) + p.o_row);
         if (!PLAIN && (s.m.ends >> i & 1)) store_state(p.hT, end_of[i] * p.D + c, h, u.mine);
     }
 }
@@ -533,25 +549,35 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
     cluster_begin(sh, cluster);
 
     uint32_t t0 = u.rank * kTile + warp * kSpan, ahead = t0;  // the warp's first token of a step, and of the next copies
+    Copies<kSpan, T> cx;
+    Copies<kSpan, G> cg;
+    if (ALIGNED) {
+        cx.start(p.x, (int64_t)u.tok0 + ahead, p.x_row, u.c0, u.cols, lane);
+        cg.start(p.g, (int64_t)u.tok0 + ahead, p.g_row, u.c0, u.cols, lane);
+    }
     const auto fetch = [&](int stage) {
         const int rows = ahead >= (uint32_t)u.S ? 0 : u.S - ahead < kSpan ? u.S - ahead : kSpan;
-        if (rows) {
+        unsigned char *to = mine + stage * kBytes;
+        if (ALIGNED && rows == kSpan) {
+            cx.span(reinterpret_cast<T *>(to), p.x_row);
+            cg.span(reinterpret_cast<G *>(to + kBytesX), p.g_row);
+        } else if (rows) {
             const int64_t tok = (int64_t)u.tok0 + ahead;
-            unsigned char *to = mine + stage * kBytes;
             copy_rows<kSpan, ALIGNED>(reinterpret_cast<T *>(to), static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
             copy_rows<kSpan, ALIGNED>(reinterpret_cast<G *>(to + kBytesX), static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
         }
         copy_commit();
         ahead += cluster * kTile;
+        if (ALIGNED) cx.src += p.x_step, cg.src += p.g_step;
     };
     for (int i = 0; i < stages; ++i) fetch(i);
     cluster_ready(cluster);
 
     Seq seq = {0, 0, 0};
     float2 carry = both(0.f);  // the state that enters the cluster's step (the last warp's)
-    T *o = static_cast<T *>(p.o) + ((int64_t)u.tok0 + t0) * p.os + c;
+    char *o = static_cast<char *>(p.o) + ((int64_t)u.tok0 + t0) * p.o_row + c * (int64_t)sizeof(T);
     const int stored = p.o ? u.mine : 0;
-    for (int step = 0, stage = 0; step < u.steps; ++step, t0 += cluster * kTile, o += (int64_t)cluster * kTile * p.os) {
+    for (int step = 0, stage = 0; step < u.steps; ++step, t0 += cluster * kTile, o += p.o_step) {
         const Span s = span_at<kSpan>(p, sh, u, t0, warp, lane, &seq);
         copy_wait(stages - 1);
         __syncwarp();
@@ -617,9 +643,9 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
         if (p.states && t0 % kSaved == 0 && s.count)
             store_state(p.states, (int64_t)(u.saved0 + t0 / kSaved) * p.D + c, h, u.mine);
         if (s.plain)
-            run_span<true, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, o);
+            run_span<true, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, reinterpret_cast<T *>(o));
         else
-            run_span<false, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, o);
+            run_span<false, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, reinterpret_cast<T *>(o));
     }
     copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
@@ -627,45 +653,52 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
 }
 
 // ---------------------------------------------------------------- backward
-// The reverse map of a span; d: its tokens' gradients in shared memory.
-template <bool PLAIN, int kSpan, typename T>
-__device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan], const T *d,
-                                           int lane, const Span &s, const int *end_of, int c) {
+// A token's two channels as they are kept in registers.
+__device__ __forceinline__ float2 raw(const float *p, int lane) { return load2(p, lane); }
+__device__ __forceinline__ __nv_bfloat162 raw(const __nv_bfloat16 *p, int lane) {
+    return reinterpret_cast<const __nv_bfloat162 *>(p)[lane];
+}
+__device__ __forceinline__ float2 value(float2 v) { return v; }
+__device__ __forceinline__ float2 value(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+
+// The reverse map of a span; d: its tokens' gradients.
+template <bool PLAIN, int kSpan, typename R>
+__device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan], const R (&d)[kSpan],
+                                           const Span &s, const int *end_of, int c) {
     float2 Y = both(0.f);
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
         if (!PLAIN && (s.m.ends >> i & 1)) Y = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
-        if (PLAIN || i < s.count) Y = mul2(a[i], add2(load2(d + i * kCh, lane), Y));
+        if (PLAIN || i < s.count) Y = mul2(a[i], add2(value(d[i]), Y));
     }
     return Y;
 }
 
-// The span's tokens: the states before them, then the gradients from the last to the first.
-template <bool PLAIN, bool COMP, bool EVEN, int kSpan, typename T, typename G>
+// The span's tokens: the states before them (minus x, COMP) in place of x, then the gradients from the
+// last to the first.
+template <bool PLAIN, bool COMP, bool EVEN, int kSpan, typename R, typename T, typename G>
 __device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                         const float2 (&w)[kSpan], const T *x, const T *d, int lane, float2 h, float2 r,
+                                         const float2 (&w)[kSpan], float2 (&x)[kSpan], const R (&d)[kSpan], float2 h, float2 r,
                                          const Span &s, const int *start_of, const int *end_of, int c, T *dx, G *dg) {
-    float2 before[kSpan];
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
         if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
-        const float2 v = load2(x + i * kCh, lane);
-        before[i] = COMP ? fma2(v, both(-1.f), h) : h;
+        const float2 v = x[i];
+        x[i] = COMP ? make_float2(h.x - v.x, h.y - v.y) : h;
         h = fma2(a[i], h, COMP ? mul2(w[i], v) : v);
     }
-    dx += (kSpan - 1) * p.dxs;
-    dg += (kSpan - 1) * p.dgs;
+    char *px = reinterpret_cast<char *>(dx) + (kSpan - 1) * p.dx_row, *pg = reinterpret_cast<char *>(dg) + (kSpan - 1) * p.dg_row;
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
         if (!PLAIN && (s.m.ends >> i & 1)) r = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
         if (PLAIN || i < s.count) {
-            const float2 e = add2(load2(d + i * kCh, lane), r);
+            const float2 e = add2(value(d[i]), r);
             r = mul2(a[i], e);
-            store_pair<EVEN>(dx, COMP ? mul2(w[i], e) : e, u.mine);
-            store_pair<EVEN>(dg, mul2(r, before[i]), u.mine);
+            store_pair<EVEN>(reinterpret_cast<T *>(px), COMP ? mul2(w[i], e) : e, u.mine);
+            store_pair<EVEN>(reinterpret_cast<G *>(pg), mul2(r, x[i]), u.mine);
         }
-        dx -= p.dxs;
-        dg -= p.dgs;
+        px -= p.dx_row;
+        pg -= p.dg_row;
         if (!PLAIN && (s.m.starts >> i & 1)) store_state(p.dh0, start_of[i] * p.D + c, r, u.mine);
     }
 }
@@ -688,11 +721,22 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
     // steps go from the stream's end
     uint32_t t0 = ((uint32_t)(u.steps - 1) * cluster + u.rank) * kTile + warp * kSpan, ahead = t0;
     int left = u.steps;  // steps whose copies are still to be made
+    Copies<kSpan, T> cx, cd;
+    Copies<kSpan, G> cg;
+    if (ALIGNED) {
+        cx.start(p.x, (int64_t)u.tok0 + ahead, p.x_row, u.c0, u.cols, lane);
+        cd.start(p.dy, (int64_t)u.tok0 + ahead, p.dy_row, u.c0, u.cols, lane);
+        cg.start(p.g, (int64_t)u.tok0 + ahead, p.g_row, u.c0, u.cols, lane);
+    }
     const auto fetch = [&](int stage) {
         const int rows = left <= 0 || ahead >= (uint32_t)u.S ? 0 : u.S - ahead < kSpan ? u.S - ahead : kSpan;
-        if (rows) {
+        unsigned char *to = mine + stage * kBytes;
+        if (ALIGNED && rows == kSpan) {
+            cx.span(reinterpret_cast<T *>(to), p.x_row);
+            cd.span(reinterpret_cast<T *>(to + kBytesX), p.dy_row);
+            cg.span(reinterpret_cast<G *>(to + 2 * kBytesX), p.g_row);
+        } else if (rows) {
             const int64_t tok = (int64_t)u.tok0 + ahead;
-            unsigned char *to = mine + stage * kBytes;
             copy_rows<kSpan, ALIGNED>(reinterpret_cast<T *>(to), static_cast<const T *>(p.x) + tok * p.xs + u.c0, p.xs, rows, u.cols, p.even, lane);
             copy_rows<kSpan, ALIGNED>(reinterpret_cast<T *>(to + kBytesX), static_cast<const T *>(p.dy) + tok * p.os + u.c0, p.os, rows, u.cols, p.even, lane);
             copy_rows<kSpan, ALIGNED>(reinterpret_cast<G *>(to + 2 * kBytesX), static_cast<const G *>(p.g) + tok * p.gs + u.c0, p.gs, rows, u.cols, p.even, lane);
@@ -700,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
         copy_commit();
         ahead -= cluster * kTile;
         --left;
+        if (ALIGNED) cx.src -= p.x_step, cd.src -= p.dy_step, cg.src -= p.g_step;
     };
     // the state that enters a step's tile (the stream's first tile starts a sequence)
     const auto saved = [&](uint32_t t) {
@@ -711,34 +756,46 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
 
     Seq seq = {0, 0, 0};
     float2 carry = both(0.f);  // the gradient of the state that leaves the step (the first warp's)
-    for (int step = 0, stage = 0; step < u.steps; ++step, t0 -= cluster * kTile) {
+    char *dx = static_cast<char *>(p.dx) + ((int64_t)u.tok0 + t0) * p.dx_row + c * (int64_t)sizeof(T);
+    char *dg = static_cast<char *>(p.dg) + ((int64_t)u.tok0 + t0) * p.dg_row + c * (int64_t)sizeof(G);
+    for (int step = 0, stage = 0; step < u.steps; ++step, t0 -= cluster * kTile, dx -= p.dx_step, dg -= p.dg_step) {
         float2 h = saved(t0);
         const Span s = span_at<kSpan>(p, sh, u, t0, warp, lane, &seq);
         copy_wait(stages - 1);
         __syncwarp();
-        const T *x = reinterpret_cast<const T *>(mine + stage * kBytes), *d = reinterpret_cast<const T *>(mine + stage * kBytes + kBytesX);
-        const G *g = reinterpret_cast<const G *>(mine + stage * kBytes + 2 * kBytesX);
+        float2 a[kSpan], w[kSpan], x[kSpan];
+        decltype(raw(static_cast<const T *>(nullptr), 0)) d[kSpan];
+        {
+            const T *xs = reinterpret_cast<const T *>(mine + stage * kBytes), *ds = reinterpret_cast<const T *>(mine + stage * kBytes + kBytesX);
+            const G *gs = reinterpret_cast<const G *>(mine + stage * kBytes + 2 * kBytesX);
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i) {
+                gate<COMP>(load2(gs + i * kCh, lane), &a[i], &w[i]);
+                x[i] = load2(xs + i * kCh, lane);
+                d[i] = raw(ds + i * kCh, lane);
+            }
+        }
+        __syncwarp();
+        fetch(stage);
+        if (++stage == stages) stage = 0;
         // the span's maps in both directions
-        float2 a[kSpan], w[kSpan], Y;
+        if (!s.plain) {
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i)
+                if (i >= s.count) a[i] = both(1.f), x[i] = both(0.f);
+        }
+        float2 Y;
         float4 f;
         {
             float2 v[kSpan];
 #pragma unroll
-            for (int i = 0; i < kSpan; ++i) {
-                const float2 gi = load2(g + i * kCh, lane);
-                gate<COMP>(gi, &a[i], &w[i]);
-                v[i] = load2(x + i * kCh, lane);
-                if (COMP) v[i] = mul2(w[i], v[i]);
-            }
+            for (int i = 0; i < kSpan; ++i) v[i] = COMP ? mul2(w[i], x[i]) : x[i];
             if (s.plain) {
                 f = map_span<true>(p, u, a, v, 0, nullptr, c);
-                Y = map_back<true>(p, u, a, d, lane, s, end_of, c);
+                Y = map_back<true>(p, u, a, d, s, end_of, c);
             } else {
-#pragma unroll
-                for (int i = 0; i < kSpan; ++i)
-                    if (i >= s.count) a[i] = both(1.f), v[i] = both(0.f);
                 f = map_span<false>(p, u, a, v, s.m.starts, start_of, c);
-                Y = map_back<false>(p, u, a, d, lane, s, end_of, c);
+                Y = map_back<false>(p, u, a, d, s, end_of, c);
             }
         }
         const bool ends = s.m.ends != 0;
@@ -793,15 +850,10 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
         __syncthreads();
         if (sh.dead) break;
         const float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
-        T *dx = static_cast<T *>(p.dx) + ((int64_t)u.tok0 + t0) * p.dxs + c;
-        G *dg = static_cast<G *>(p.dg) + ((int64_t)u.tok0 + t0) * p.dgs + c;
         if (s.plain)
-            run_back<true, COMP, ALIGNED>(p, u, a, w, x, d, lane, h, r, s, start_of, end_of, c, dx, dg);
+            run_back<true, COMP, ALIGNED>(p, u, a, w, x, d, h, r, s, start_of, end_of, c, reinterpret_cast<T *>(dx), reinterpret_cast<G *>(dg));
         else
-            run_back<false, COMP, ALIGNED>(p, u, a, w, x, d, lane, h, r, s, start_of, end_of, c, dx, dg);
-        __syncwarp();
-        fetch(stage);
-        if (++stage == stages) stage = 0;
+            run_back<false, COMP, ALIGNED>(p, u, a, w, x, d, h, r, s, start_of, end_of, c, reinterpret_cast<T *>(dx), reinterpret_cast<G *>(dg));
     }
     copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
@@ -915,6 +967,10 @@ cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
     if (stages > steps) stages = steps;
     p.stages = stages < 1 ? 1 : (int32_t)stages;
     const size_t smem = bytes * p.stages + maps;
+    const int64_t es = sizeof(T), ges = sizeof(G), tokens = (int64_t)p.cluster * tile;
+    p.x_row = p.xs * es, p.g_row = p.gs * ges, p.dy_row = p.o_row = p.os * es, p.dx_row = p.dxs * es, p.dg_row = p.dgs * ges;
+    p.x_step = tokens * p.x_row, p.g_step = tokens * p.g_row, p.dy_step = p.o_step = tokens * p.o_row;
+    p.dx_step = tokens * p.dx_row, p.dg_step = tokens * p.dg_row;
     p.wait_limit = call_wait_limit();
     p.test_hook = call_test_hook();
     GDN_LAUNCH(fwd ? kKLinrecFwd : kKLinrecBwd, s, (err = launch_cluster(kernel, p, smem, s)));
