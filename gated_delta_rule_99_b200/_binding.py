@@ -323,6 +323,9 @@ def _scope(first, stream, used):
 
 
 def _like(t):
+    """An empty contiguous tensor of this shape and type (the format given costs a microsecond)."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 

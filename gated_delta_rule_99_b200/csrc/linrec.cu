@@ -8,10 +8,10 @@
 // one span per warp, whose factors and inputs stay in registers.  Each of eight warps forms its
 // span's map and joins the maps of the spans before it; the last one, which thereby has the
 // tile's map, carries the state.  A cluster of up to 16 CTAs takes consecutive tiles of the
-// same channels: the carrying warps send their tile's map to all of them (one bulk copy each
-// through distributed shared memory, counted by an mbarrier: a cluster barrier's release
-// would wait for the outputs still being stored) and each folds them in order, so each holds
-// the state that enters its tile and the next step.  The data is read from memory once, by
+// same channels: the carrying warps send their tile's map to all of them (st.async through
+// distributed shared memory, counted by an mbarrier: a release would wait for the outputs
+// still being stored) and each folds them in order, so each holds the state that enters its
+// tile and the next step.  The data is read from memory once, by
 // cp.async into a ring of tiles that runs ahead of the steps, each warp copying its own rows.
 //
 // A start of a sequence inside a span drops what comes before it by selection (not by a
@@ -239,10 +239,10 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
-// Copies shared memory into a CTA of the cluster; its bytes count down that CTA's mbarrier.
-__device__ __forceinline__ void send(uint32_t to, const void *from, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(to), "r"(smem_addr(from)), "r"(bytes), "r"(bar) : "memory");
+// Stores 16 bytes into a CTA of the cluster; they count down its mbarrier.
+__device__ __forceinline__ void send(uint32_t to, float4 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar) : "memory");
 }
 
 // Status of this device's calls (gdn_linrec_status).
@@ -385,10 +385,11 @@ __device__ __forceinline__ void pass_empty(const LinrecParams &p, const Unit &u,
 }
 
 // ---------------------------------------------------------------- the carrying warp
-// A tile's map; a step's maps, and those of the step before it, are in each CTA of the cluster.
+// A tile's map (A, X of each lane's two channels); a step's maps, and those of the step before it, are
+// in each CTA of the cluster.  Factors are not negative, so the sign of the first one says that
+// what comes before the tile does not count.
 struct __align__(16) Map {
     float4 m[32];
-    int cut, pad[3];
 };
 // Shared memory of a CTA, beside its tiles and the cluster's maps.
 struct Shared {
@@ -399,7 +400,6 @@ struct Shared {
     int cut[kWarps];                        // bit 0: a start in the span, bit 1: an end
     int start_of[kWarps][kMaxSpan], end_of[kWarps][kMaxSpan];
     int dead;                               // a wait ran out
-    Map out[2];                             // the tile's map on its way to the cluster (even, odd steps)
 };
 __device__ __forceinline__ float2 join(float4 s, bool cut, float2 h) {
     return cut ? make_float2(s.y, s.w) : fma2(make_float2(s.x, s.z), h, make_float2(s.y, s.w));
@@ -449,16 +449,16 @@ __device__ __forceinline__ void cluster_end(int cluster) {
 __device__ __forceinline__ void send_map(const LinrecParams &p, Shared &sh, Map *maps, int rank, int step, int lane, float4 q, bool cut) {
     if (p.cluster == 1) return;
     const int buf = step & 1;
-    Map *to = maps + buf * p.cluster + rank, *out = &sh.out[buf];
-    out->m[lane] = q;
     if (lane == 0) {
-        out->cut = cut;
         const bool stall = p.test_hook == GDN_TEST_STALL_COPY && blockIdx.x == 0 && step == 0;
         ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * (uint32_t)sizeof(Map) + (stall ? 16 : 0));
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane < p.cluster) send(cluster_addr(to, lane), out, sizeof(Map), cluster_addr(&sh.bar[buf], lane));
+    if (cut) q.x = -0.f;
+    const Map *to = maps + buf * p.cluster + rank;
+    for (int i = 1; i <= p.cluster; ++i) {  // to the neighbour first, so that no CTA is everyone's first
+        const int r = rank + i < p.cluster ? rank + i : rank + i - p.cluster;
+        send(cluster_addr(&to->m[lane], r), q, cluster_addr(&sh.bar[buf], r));
+    }
 }
 template <bool REV>
 __device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, const Map *maps, int rank, int step, int lane, float4 q, bool cut, float2 *carry) {
@@ -474,11 +474,19 @@ __device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, cons
     }
     const Map *from = maps + buf * p.cluster;
     float2 c = *carry;
-#pragma unroll 4
-    for (int i = 0; i < p.cluster; ++i) {
-        const int j = REV ? p.cluster - 1 - i : i;
-        if (j == rank) sh.enter[lane] = c;
-        c = join(from[j].m[lane], from[j].cut, c);
+    for (int i0 = 0; i0 < p.cluster; i0 += 4) {  // four loads at a time
+        float4 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = i0 + i < p.cluster ? i0 + i : 0;
+            f[i] = from[REV ? p.cluster - 1 - k : k].m[lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= p.cluster) break;
+            if ((REV ? p.cluster - 1 - (i0 + i) : i0 + i) == rank) sh.enter[lane] = c;
+            c = join(f[i], signbit(f[i].x), c);
+        }
     }
     *carry = c;
 }
