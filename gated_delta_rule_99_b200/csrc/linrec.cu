@@ -869,25 +869,60 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
 }
 
 // ---------------------------------------------------------------- one-token form
-__device__ __forceinline__ float ld(const float *p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float ld(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
-
-template <typename T, typename G, bool COMP>
-__global__ void __launch_bounds__(128) linrec_decode_kernel(LinrecParams p, float *state) {
-    const int64_t c = (int64_t)blockIdx.y * 128 + threadIdx.x, n = blockIdx.x;
-    if (c >= p.D) return;
-    const T *x = static_cast<const T *>(p.x);
-    const G *g = static_cast<const G *>(p.g);
-    T *o = static_cast<T *>(p.o);
-    float h = state[n * p.D + c];
-    for (int64_t t = n * p.T; t < (n + 1) * p.T; ++t) {
-        const float gt = ld(g, t * p.gs + c), xt = ld(x, t * p.xs + c);
-        float2 a, w;
-        gate<COMP>(make_float2(gt, 0.f), &a, &w);
-        h = fmaf(a.x, h, COMP ? w.x * xt : xt);
-        put(o + t * p.os + c, h);
+// C adjacent channels per thread (4 where rows and states allow 16-byte state accesses, else 1), the
+// state in registers over the T tokens.  Bound by the state's bytes for many rows, by the launch
+// for few: back to back 1.7 us for 256 x 2048 bf16 (3.5 us with a channel per thread), 1.1 us for 1 x 2048.
+template <int C>
+__device__ __forceinline__ void load_some(const float *p, float (&v)[C]) {
+    if (C == 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(p);
+        v[0] = t.x, v[1 % C] = t.y, v[2 % C] = t.z, v[3 % C] = t.w;
+    } else {
+        v[0] = *p;
     }
-    state[n * p.D + c] = h;
+}
+template <int C>
+__device__ __forceinline__ void load_some(const __nv_bfloat16 *p, float (&v)[C]) {
+    if (C == 4) {
+        const uint2 t = *reinterpret_cast<const uint2 *>(p);
+        v[0] = __uint_as_float(t.x << 16), v[1 % C] = __uint_as_float(t.x & 0xffff0000u);
+        v[2 % C] = __uint_as_float(t.y << 16), v[3 % C] = __uint_as_float(t.y & 0xffff0000u);
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
+}
+template <typename T, typename G, bool COMP, int C>
+__global__ void __launch_bounds__(128) linrec_decode_kernel(const __grid_constant__ LinrecParams p, float *state) {
+    const int64_t c = ((int64_t)blockIdx.y * 128 + threadIdx.x) * C, n = blockIdx.x;
+    if (c >= p.D) return;
+    const T *x = static_cast<const T *>(p.x) + n * p.T * p.xs + c;
+    const G *g = static_cast<const G *>(p.g) + n * p.T * p.gs + c;
+    T *o = static_cast<T *>(p.o) + n * p.T * p.os + c;
+    float h[C];
+    load_some<C>(state + n * p.D + c, h);
+    for (int64_t t = 0; t < p.T; ++t, x += p.xs, g += p.gs, o += p.os) {
+        float xt[C], gt[C];
+        load_some<C>(x, xt);
+        load_some<C>(g, gt);
+#pragma unroll
+        for (int i = 0; i < C; i += 2) {
+            float2 a, w;
+            gate<COMP>(make_float2(gt[i], gt[(i + 1) % C]), &a, &w);
+            h[i] = fmaf(a.x, h[i], COMP ? w.x * xt[i] : xt[i]);
+            if (C > 1) h[(i + 1) % C] = fmaf(a.y, h[(i + 1) % C], COMP ? w.y * xt[(i + 1) % C] : xt[(i + 1) % C]);
+        }
+        if (C > 1) {
+#pragma unroll
+            for (int i = 0; i < C; i += 2) put2(o + i, make_float2(h[i], h[(i + 1) % C]));
+        } else {
+            put(o, h[0]);
+        }
+    }
+    float *to = state + n * p.D + c;
+    if (C == 4)
+        *reinterpret_cast<float4 *>(to) = make_float4(h[0], h[1 % C], h[2 % C], h[3 % C]);
+    else
+        *to = h[0];
 }
 
 // ---------------------------------------------------------------- launches
@@ -988,8 +1023,13 @@ cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
 template <typename T, typename G, bool COMP>
 cudaError_t launch_even(const LinrecParams &p, Pass pass, float *state, cudaStream_t s) {
     if (pass == Pass::kDecode) {
-        const dim3 grid((unsigned)p.N, (unsigned)((p.D + 127) / 128));
-        GDN_LAUNCH(kKLinrecDecode, s, linrec_decode_kernel<T, G, COMP><<<grid, 128, 0, s>>>(p, state));
+        const bool fours = (p.D | p.xs | p.gs | p.os) % 4 == 0;
+        const int64_t width = fours ? 512 : 128;
+        const dim3 grid((unsigned)p.N, (unsigned)((p.D + width - 1) / width));
+        if (fours)
+            GDN_LAUNCH(kKLinrecDecode, s, linrec_decode_kernel<T, G, COMP, 4><<<grid, 128, 0, s>>>(p, state));
+        else
+            GDN_LAUNCH(kKLinrecDecode, s, linrec_decode_kernel<T, G, COMP, 1><<<grid, 128, 0, s>>>(p, state));
         return cudaSuccess;
     }
     return p.aligned ? launch_typed<T, G, COMP, true>(p, pass, s) : launch_typed<T, G, COMP, false>(p, pass, s);
