@@ -681,6 +681,60 @@ def run_report(args, rank, world, local_rank):
                 "peaks": pk["src"]}), flush=True)
         del d, ws, o, hT, grads
         torch.cuda.empty_cache()
+    if rank == 0:
+        report_operators(pk, flush, max(5, args.steps))
+
+
+def report_operators(pk, flush, steps):
+    """The report's rows for the operators around the layer: the gated linear recurrence (at the
+    widths of the workloads: 16 or 8 heads x 128 channels) and the q/k normalisation with rotation.
+    All are bound by the bytes that a call cannot do without."""
+    import torch
+
+    import gated_delta_rule_99_b200 as gdn
+    dev = flush.device
+    gen = torch.Generator(device=dev).manual_seed(70)
+    r = lambda *s: torch.randn(*s, generator=gen, device=dev)
+
+    def row(name, what, tokens, nbytes, call):
+        for _ in range(3):
+            call()
+        evs = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+               for _ in range(steps)]
+        torch.cuda.synchronize()
+        for a, b in evs:
+            flush.zero_()
+            a.record()
+            call()
+            b.record()
+        torch.cuda.synchronize()
+        ms = sum(a.elapsed_time(b) for a, b in evs) / steps
+        bound = nbytes / (pk["hbm"] * 1e9)
+        print(json.dumps({"workload": name, "pass": what, "tokens_per_s": tokens / (ms / 1e3),
+                          "ms_per_call": ms, "roofline_frac": bound * 1e3 / ms,
+                          "roofline_us": bound * 1e6, "path": "cuda-core fp32", "peaks": pk["src"]}),
+              flush=True)
+
+    for B, T, D in ((4, 4096, 2048), (1, 1 << 18, 1024)):
+        n = B * T * D
+        x, g, do = r(B, T, D).bfloat16(), -torch.rand(B, T, D, generator=gen, device=dev) * 0.1, r(B, T, D).bfloat16()
+        o, dx, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(g)
+        states = gdn.gdn_linrec_fwd(x, g, o=o, save_states=True)[2]
+        name = "linrec_bf16_B%d_T%d_D%d" % (B, T, D)
+        row(name, "fwd", B * T, n * 8, lambda: gdn.gdn_linrec_fwd(x, g, o=o, states=states))
+        row(name, "bwd", B * T, n * 14,
+            lambda: gdn.gdn_linrec_bwd(x, g, do, states=states, grads=(dx, dg, None)))
+        if gdn.linrec_status() != 0:
+            raise RuntimeError("device status not ok (%s)" % name)
+    q, k = r(4, 4096, 16, 128).bfloat16(), r(4, 4096, 16, 128).bfloat16()
+    w, f = torch.ones(128, device=dev), torch.rand(64, generator=gen, device=dev)
+    out = [torch.empty_like(q) for _ in range(4)] + [torch.empty_like(w) for _ in range(2)]
+    ws = gdn.alloc_workspace(1 << 20, dev)
+    kw = dict(inv_freq=f, q_weight=w, k_weight=w)
+    row("qk_norm_rope_bf16_B4_T4096_H16_d128", "fwd", 4 * 4096, 4 * q.numel() * 2,
+        lambda: gdn.gdn_qk_norm_rope_fwd(q, k, qo=out[0], ko=out[1], **kw))
+    row("qk_norm_rope_bf16_B4_T4096_H16_d128", "bwd", 4 * 4096, 6 * q.numel() * 2,
+        lambda: gdn.gdn_qk_norm_rope_bwd(q, k, out[0], out[1], grads=tuple(out[2:]), workspace=ws, **kw))
 
 
 def main():

@@ -90,6 +90,75 @@ def test_many_documents_of_odd_lengths():
     run_and_check(draw(1, sum(lengths), 40, N=150, seed=3), lengths=lengths)
 
 
+def test_thousands_of_documents_of_no_one_or_a_few_tokens():
+    """Longer searches for a token's document, in both directions, and long runs of empty ones."""
+    rng = np.random.default_rng(8)
+    lengths = [int(n) for n in rng.choice([0, 0, 0, 0, 1, 2, 40], size=4000)]
+    lengths[100:1500] = [0] * 1400
+    run_and_check(draw(1, sum(lengths), 8, N=4000, seed=8), lengths=lengths)
+
+
+def test_rows_of_no_token():
+    x = torch.zeros(3, 0, 40, device="cuda")
+    h0, dhT = torch.randn(3, 40, device="cuda"), torch.randn(3, 40, device="cuda")
+    assert torch.equal(gdn.gdn_linrec_fwd(x, x, h0=h0)[1], h0)
+    assert torch.equal(gdn.gdn_linrec_bwd(x, x, x, dhT=dhT)[2], dhT)
+    assert (gdn.gdn_linrec_fwd(x, x)[1] == 0).all()
+
+
+def test_one_token_slices_of_a_batch_of_rows():
+    """x[:, t:t + 1] of (B, T, D): tokens a whole row apart."""
+    v = draw(5, 7, 64, seed=14)
+    x, g = v["x"].cuda(), v["g"].cuda()
+    a, b = v["h0"].cuda(), v["h0"].cuda()
+    for t in range(7):
+        o = gdn.gdn_linrec_decode(x[:, t:t + 1], g[:, t:t + 1], a)
+        want = gdn.gdn_linrec_decode(x[:, t:t + 1].contiguous(), g[:, t:t + 1].contiguous(), b)
+        assert torch.equal(o, want) and torch.equal(a, b)
+    for got, want in zip(gdn.gdn_linrec_fwd(x[:, 3:4], g[:, 3:4]),
+                         gdn.gdn_linrec_fwd(x[:, 3:4].contiguous(), g[:, 3:4].contiguous())):
+        assert torch.equal(got, want)
+
+
+def test_long_memory_keeps_its_precision():
+    """Factors around 0.999: an exponential that is low by a fraction of an ulp on average would show
+    in a state that sums up thousands of tokens.  Bound: rounding of every step, one ulp each, in
+    the same direction for no more than the memory's length: 2^-23 / (1 - 0.999) = 1.2e-4 of the
+    sum of magnitudes is certain; unbiased roundings add up like their square root, 4e-6, and ten
+    times less than the former is asked for."""
+    T = 20000
+    gen = torch.Generator().manual_seed(2)
+    g = -torch.rand(1, T, 64, generator=gen) * 0.002
+    x = torch.ones(1, T, 64)
+    o, hT = gdn.gdn_linrec_fwd(x.cuda(), g.cuda())
+    want = np.zeros(64)
+    for a in np.exp(np64(g)[0]):
+        want = a * want + 1
+    assert (np.abs(np64(hT)[0] - want) <= 1.2e-5 * want).all()
+
+
+def test_two_host_threads():
+    from concurrent.futures import ThreadPoolExecutor
+    v = [draw(2, 300, 72, seed=s) for s in (40, 41)]
+    want = [run_and_check(a) for a in v]
+    dev = [{k: t.cuda() for k, t in a.items()} for a in v]
+    torch.cuda.synchronize()
+
+    def work(i):
+        d = dev[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                out = gdn.gdn_linrec_fwd(d["x"], d["g"], h0=d["h0"])
+                out += gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], h0=d["h0"], dhT=d["dhT"])
+            torch.cuda.current_stream().synchronize()
+        return out
+
+    with ThreadPoolExecutor(2) as pool:
+        for got, expected in zip(pool.map(work, (0, 1)), want):
+            for a, b in zip(got, expected):
+                assert torch.equal(a, b)
+
+
 def test_no_initial_and_final_states():
     v = draw(2, 200, 48, state=False)
     args = {k: t.cuda() for k, t in v.items() if t is not None}

@@ -71,7 +71,8 @@ def run_and_check(v, norm="rms", eps=None, interleaved=False, on=lambda t: t.cud
 @pytest.mark.parametrize("norm", ["rms", "l2", None])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("d,rot", [(128, 128), (128, 64), (64, 64), (256, 256), (2, 2), (10, 6), (80, 80),
-                                   (96, 48), (192, 20), (66, 34), (16, 0), (250, 250)])
+                                   (96, 48), (192, 20), (66, 34), (16, 0), (250, 250), (80, 40), (12, 8),
+                                   (100, 36), (256, 2), (256, 40)])
 def test_row_sizes(d, rot, interleaved, norm, dtype):
     v = draw(2, 5, 3, 2, d, rot, dtype, weights=norm != "l2", seed=d + rot)
     run_and_check(v, norm, interleaved=interleaved)
@@ -161,6 +162,16 @@ def test_column_slices_of_one_projection(d, pad):
         assert torch.equal(p, t)
         n = p.shape[2] * d
         assert (w[..., :8] == 7).all() and (w[..., 8 + n:] == 7).all()
+
+
+def test_one_token_slices_of_a_batch_of_rows():
+    v = draw(5, 3, 2, 1, 64, 64)
+    q, k, f = v["q"].cuda(), v["k"].cuda(), v["inv_freq"].cuda()
+    pos = torch.tensor([[7], [0], [1 << 20], [3], [9]], dtype=torch.int32, device="cuda")
+    for t in range(3):
+        got = gdn.gdn_qk_norm_rope_fwd(q[:, t:t + 1], k[:, t:t + 1], f, pos)
+        want = gdn.gdn_qk_norm_rope_fwd(q[:, t:t + 1].contiguous(), k[:, t:t + 1].contiguous(), f, pos)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_gradients_against_differences():
