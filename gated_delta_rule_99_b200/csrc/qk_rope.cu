@@ -11,6 +11,10 @@
 // shared memory by all its heads.  Bound by HBM: every row is read and written once.  The
 // weights' gradients are summed in registers over a block's rows, written once per block, and
 // added in block order by a second kernel.
+//
+// Measured for 4 x 4096 tokens of 16 + 16 heads x 128: bf16 56 us forward and 90 us backward (73% and
+// 69% of the measured copy rate, bound by the instructions: 65% of the issue slots), fp32 90 and
+// 136 us (90%).  With a warp per row and shared memory between the passes: 335 and 560 us.
 #include <cmath>
 
 #include "gdn_internal.cuh"
@@ -19,8 +23,8 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxD = 256, kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSms = 148, kPerSm = 3, kBwdPerSm = 2;            // blocks of an SM
-constexpr int kSlots = kSms * kPerSm;           // blocks at most, of both tensors
+constexpr int kSms = 148, kPerSm = 3, kBwdPerSm = 2;  // blocks of an SM
+constexpr int kSlots = kSms * kPerSm;  // blocks at most, of both tensors
 
 struct QkParams {
     int64_t tokens;
@@ -199,7 +203,9 @@ struct Way {
 // NU units per lane.  VEC: whole chunks are loaded and stored at once.
 template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD>
 __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
-    constexpr int kUnroll = NU > 1 ? 1 : BWD ? 1 : 2;
+    // rows on their way: two, but one in the backward of bf16 rows, whose registers a second one spills (90
+    // against 95 us for 4 x 4096 tokens of 16 + 16 heads x 128; fp32: 152 against 136 us the other way)
+    constexpr int kUnroll = NU > 1 || (BWD && sizeof(T) == 2) ? 1 : 2;
     __shared__ __align__(16) float2 angles[kWarps][kMaxD / 2 + 8];  // (cos, sin), see angle_at
     __shared__ float sums[BWD ? kWarps : 1][kMaxD];
     __shared__ __align__(16) float weights[kMaxD];
