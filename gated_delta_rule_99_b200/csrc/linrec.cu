@@ -37,7 +37,8 @@ constexpr int kCh = 64;        // channels per CTA
 constexpr int kSaved = 64;     // tokens between two saved states
 constexpr int kMaxSpan = 16, kMaxStages = 8, kMaxCluster = 16;
 constexpr int kFwdPerSm = 2, kBwdPerSm = 2;  // CTAs per SM that the registers allow
-constexpr size_t kSmemSm = 227 * 1024, kSmemCta = 9 * 1024 + 512;  // of an SM, and of a CTA beside tiles and maps
+constexpr size_t kSmemSm = 227 * 1024;  // of an SM
+constexpr int kCuKept = 256;                // offsets of documents that a CTA keeps
 
 // Tokens per warp: 16 in the forward of bf16 inputs; 8 where the tiles are larger, and in the
 // backward, which has more to keep in registers.
@@ -257,9 +258,9 @@ struct Seq {
 // Moves s to the sequence that holds token t (0 <= t < S).  Packed: the largest n with cu[n]
 // <= t, searched near s first and then 33 ways at a time.  Only cu[1 .. N - 1] are trusted as
 // far as indices go; the bounds are forced around t whatever they hold.
-__device__ __forceinline__ void seek(const LinrecParams &p, int first, int S, int t, int lane, Seq *s) {
+__device__ __forceinline__ void seek(const LinrecParams &p, const int32_t *cu, int first, int S, int t, int lane, Seq *s) {
     if (t >= s->beg && t < s->end) return;
-    if (!p.cu) {
+    if (!cu) {
         const int T = (int)p.T, k = t / T;
         s->n = first + k, s->beg = k * T, s->end = s->beg + T;
         return;
@@ -271,7 +272,7 @@ __device__ __forceinline__ void seek(const LinrecParams &p, int first, int S, in
     } else {
         hi = s->n > 0 ? s->n : 1;
         const int at = hi - 1 - lane;
-        const bool after = at > lo && p.cu[at] > t;
+        const bool after = at > lo && cu[at] > t;
         const int cnt = __ffs(~__ballot_sync(0xffffffffu, after)) - 1;  // -1: all 32
         if (cnt >= 0) {
             hi -= cnt;
@@ -283,7 +284,7 @@ __device__ __forceinline__ void seek(const LinrecParams &p, int first, int S, in
     }
     while (hi - lo > 1) {
         const int64_t at = lo + (int64_t)(lane + 1) * step;
-        const bool before = at < hi && p.cu[at] <= t;
+        const bool before = at < hi && cu[at] <= t;
         const uint32_t b = __ballot_sync(0xffffffffu, before);
         const int cnt = b == 0xffffffffu ? 32 : __ffs(~b) - 1;
         const int64_t end = lo + (int64_t)(cnt + 1) * step;
@@ -291,7 +292,7 @@ __device__ __forceinline__ void seek(const LinrecParams &p, int first, int S, in
         if (cnt < 32 && end < hi) hi = (int)end;
         step = (hi - lo + 32) / 33;
     }
-    const int b = lo > 0 ? p.cu[lo] : 0, e = lo + 1 < (int)p.N ? p.cu[lo + 1] : S;
+    const int b = lo > 0 ? cu[lo] : 0, e = lo + 1 < (int)p.N ? cu[lo + 1] : S;
     s->n = lo;
     s->beg = b < 0 ? 0 : b > t ? t : b;
     s->end = e > S ? S : e <= t ? t + 1 : e;
@@ -303,7 +304,7 @@ __device__ __forceinline__ void seek(const LinrecParams &p, int first, int S, in
 struct Marks {
     uint32_t starts, ends;
 };
-__device__ __forceinline__ Marks mark(const LinrecParams &p, int first, int S, int t0, int t1, int lane,
+__device__ __forceinline__ Marks mark(const LinrecParams &p, const int32_t *cu, int first, int S, int t0, int t1, int lane,
                                       Seq *s, int *start_of, int *end_of) {
     Marks m = {0, 0};
     if (t0 >= t1) return m;
@@ -316,7 +317,7 @@ __device__ __forceinline__ Marks mark(const LinrecParams &p, int first, int S, i
         }
         return m;
     }
-    seek(p, first, S, t0, lane, s);
+    seek(p, cu, first, S, t0, lane, s);
     Seq q = *s;
     if (q.beg == t0) {
         m.starts = 1;
@@ -329,7 +330,7 @@ __device__ __forceinline__ Marks mark(const LinrecParams &p, int first, int S, i
             if (lane == 0) end_of[e - 1 - t0] = q.n;
         }
         if (e >= t1) break;
-        seek(p, first, S, e, lane, &q);
+        seek(p, cu, first, S, e, lane, &q);
         m.starts |= 1u << (e - t0);
         if (lane == 0) start_of[e - t0] = q.n;
     }
@@ -400,7 +401,10 @@ struct Shared {
     int cut[kWarps];                        // bit 0: a start in the span, bit 1: an end
     int start_of[kWarps][kMaxSpan], end_of[kWarps][kMaxSpan];
     int dead;                               // a wait ran out
+    int32_t cu[kCuKept];                    // the offsets of few documents: crossing one costs no global loads
 };
+constexpr size_t kSmemCta = sizeof(Shared) + 1024;  // of a CTA beside tiles and maps (1 KB is the system's)
+
 __device__ __forceinline__ float2 join(float4 s, bool cut, float2 h) {
     return cut ? make_float2(s.y, s.w) : fma2(make_float2(s.x, s.z), h, make_float2(s.y, s.w));
 }
@@ -423,7 +427,9 @@ __device__ __forceinline__ void give_up(Shared &sh) {
 }
 
 // Makes the mbarriers ready in every CTA of the cluster before anyone sends.
-__device__ __forceinline__ void cluster_begin(Shared &sh, int cluster) {
+__device__ __forceinline__ void cluster_begin(const LinrecParams &p, Shared &sh, int cluster) {
+    if (p.cu && p.N < kCuKept)
+        for (int i = threadIdx.x; i <= p.N; i += kThreads) sh.cu[i] = p.cu[i];
     if (threadIdx.x == 0) {
         sh.dead = 0;
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.bar[i], 1);
@@ -504,22 +510,37 @@ __device__ __forceinline__ Span span_at(const LinrecParams &p, Shared &sh, const
     if (p.single ? t0 > 0 && t0 + kSpan < (uint32_t)u.S : (int)t0 > seq->beg && t0 + kSpan < (uint32_t)seq->end) return s;
     s.count = t0 >= (uint32_t)u.S ? 0 : u.S - t0 < kSpan ? u.S - t0 : kSpan;
     __syncwarp();
-    if (s.count) s.m = mark(p, u.first, u.S, (int)t0, (int)t0 + s.count, lane, seq, sh.start_of[warp], sh.end_of[warp]);
+    if (s.count) s.m = mark(p, p.N < kCuKept && p.cu ? sh.cu : p.cu, u.first, u.S, (int)t0, (int)t0 + s.count, lane, seq, sh.start_of[warp], sh.end_of[warp]);
     s.plain = !(s.m.starts | s.m.ends) && s.count == kSpan;
     __syncwarp();
     return s;
+}
+
+// A state that a span reads, asked for before the span's copies are waited for: that of the first
+// start (or last end) in it.
+struct Early {
+    int i;  // the token in the span, -1: none
+    float2 v;
+};
+__device__ __forceinline__ Early early(const float *p, const LinrecParams &q, const Unit &u, int i, const int *of, int c) {
+    Early e = {i, both(0.f)};
+    if (i >= 0) e.v = load_state(p, of[i] * q.D + c, u.mine);
+    return e;
+}
+__device__ __forceinline__ float2 state_at(const Early &e, const float *p, const LinrecParams &q, const Unit &u, int i, const int *of, int c) {
+    return i == e.i ? e.v : load_state(p, of[i] * q.D + c, u.mine);
 }
 
 // ---------------------------------------------------------------- forward
 // A span's map.  PLAIN: no sequence starts in it.
 template <bool PLAIN, int kSpan>
 __device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
-                                           const float2 (&v)[kSpan], uint32_t starts, const int *start_of, int c) {
+                                           const float2 (&v)[kSpan], uint32_t starts, const Early &e, const int *start_of, int c) {
     float2 A = a[0], X = v[0];
-    if (!PLAIN && (starts & 1)) X = fma2(a[0], load_state(p.h0, start_of[0] * p.D + c, u.mine), v[0]);
+    if (!PLAIN && (starts & 1)) X = fma2(a[0], state_at(e, p.h0, p, u, 0, start_of, c), v[0]);
 #pragma unroll
     for (int i = 1; i < kSpan; ++i) {
-        if (!PLAIN && (starts >> i & 1)) X = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        if (!PLAIN && (starts >> i & 1)) X = state_at(e, p.h0, p, u, i, start_of, c);
         X = fma2(a[i], X, v[i]);
         A = mul2(A, a[i]);
     }
@@ -530,10 +551,10 @@ __device__ __forceinline__ float4 map_span(const LinrecParams &p, const Unit &u,
 template <bool PLAIN, bool EVEN, int kSpan, typename T>
 __device__ __forceinline__ void run_span(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
                                          const float2 (&v)[kSpan], float2 h, const Span &s, int mine,
-                                         const int *start_of, const int *end_of, int c, T *o) {
+                                         const Early &e, const int *start_of, const int *end_of, int c, T *o) {
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
-        if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        if (!PLAIN && (s.m.starts >> i & 1)) h = state_at(e, p.h0, p, u, i, start_of, c);
         h = fma2(a[i], h, v[i]);
         if (PLAIN || i < s.count) store_pair<EVEN>(o, h, mine);
         o = reinterpret_cast<T *>(reinterpret_cast<char *>(o) + p.o_row);
@@ -554,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
     unsigned char *mine = smem + warp * stages * kBytes;
     Map *maps = reinterpret_cast<Map *>(smem + kWarps * stages * kBytes);
     const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
-    cluster_begin(sh, cluster);
+    cluster_begin(p, sh, cluster);
 
     uint32_t t0 = u.rank * kTile + warp * kSpan, ahead = t0;  // the warp's first token of a step, and of the next copies
     Copies<kSpan, T> cx;
@@ -587,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
     const int stored = p.o ? u.mine : 0;
     for (int step = 0, stage = 0; step < u.steps; ++step, t0 += cluster * kTile, o += p.o_step) {
         const Span s = span_at<kSpan>(p, sh, u, t0, warp, lane, &seq);
+        const Early e = early(p.h0, p, u, __ffs(s.m.starts) - 1, start_of, c);
         copy_wait(stages - 1);
         __syncwarp();
         float2 a[kSpan], v[kSpan];
@@ -607,12 +629,12 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
         if (++stage == stages) stage = 0;
         float4 own;
         if (s.plain) {
-            own = map_span<true>(p, u, a, v, 0, nullptr, c);
+            own = map_span<true>(p, u, a, v, 0, e, nullptr, c);
         } else {
 #pragma unroll
             for (int i = 0; i < kSpan; ++i)
                 if (i >= s.count) a[i] = both(1.f), v[i] = both(0.f);
-            own = map_span<false>(p, u, a, v, s.m.starts, start_of, c);
+            own = map_span<false>(p, u, a, v, s.m.starts, e, start_of, c);
         }
         const bool cuts = s.m.starts != 0;
         sh.spans[warp][lane] = own;
@@ -651,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const _
         if (p.states && t0 % kSaved == 0 && s.count)
             store_state(p.states, (int64_t)(u.saved0 + t0 / kSaved) * p.D + c, h, u.mine);
         if (s.plain)
-            run_span<true, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, reinterpret_cast<T *>(o));
+            run_span<true, ALIGNED>(p, u, a, v, h, s, stored, e, start_of, end_of, c, reinterpret_cast<T *>(o));
         else
-            run_span<false, ALIGNED>(p, u, a, v, h, s, stored, start_of, end_of, c, reinterpret_cast<T *>(o));
+            run_span<false, ALIGNED>(p, u, a, v, h, s, stored, e, start_of, end_of, c, reinterpret_cast<T *>(o));
     }
     copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
@@ -672,11 +694,11 @@ __device__ __forceinline__ float2 value(__nv_bfloat162 v) { return __bfloat1622f
 // The reverse map of a span; d: its tokens' gradients.
 template <bool PLAIN, int kSpan, typename R>
 __device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan], const R (&d)[kSpan],
-                                           const Span &s, const int *end_of, int c) {
+                                           const Span &s, const Early &l, const int *end_of, int c) {
     float2 Y = both(0.f);
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
-        if (!PLAIN && (s.m.ends >> i & 1)) Y = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
+        if (!PLAIN && (s.m.ends >> i & 1)) Y = state_at(l, p.dhT, p, u, i, end_of, c);
         if (PLAIN || i < s.count) Y = mul2(a[i], add2(value(d[i]), Y));
     }
     return Y;
@@ -687,10 +709,10 @@ __device__ __forceinline__ float2 map_back(const LinrecParams &p, const Unit &u,
 template <bool PLAIN, bool COMP, bool EVEN, int kSpan, typename R, typename T, typename G>
 __device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, const float2 (&a)[kSpan],
                                          const float2 (&w)[kSpan], float2 (&x)[kSpan], const R (&d)[kSpan], float2 h, float2 r,
-                                         const Span &s, const int *start_of, const int *end_of, int c, T *dx, G *dg) {
+                                         const Span &s, const Early &e, const Early &l, const int *start_of, const int *end_of, int c, T *dx, G *dg) {
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
-        if (!PLAIN && (s.m.starts >> i & 1)) h = load_state(p.h0, start_of[i] * p.D + c, u.mine);
+        if (!PLAIN && (s.m.starts >> i & 1)) h = state_at(e, p.h0, p, u, i, start_of, c);
         const float2 v = x[i];
         x[i] = COMP ? make_float2(h.x - v.x, h.y - v.y) : h;
         h = fma2(a[i], h, COMP ? mul2(w[i], v) : v);
@@ -698,11 +720,11 @@ __device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, c
     char *px = reinterpret_cast<char *>(dx) + (kSpan - 1) * p.dx_row, *pg = reinterpret_cast<char *>(dg) + (kSpan - 1) * p.dg_row;
 #pragma unroll
     for (int i = kSpan - 1; i >= 0; --i) {
-        if (!PLAIN && (s.m.ends >> i & 1)) r = load_state(p.dhT, end_of[i] * p.D + c, u.mine);
+        if (!PLAIN && (s.m.ends >> i & 1)) r = state_at(l, p.dhT, p, u, i, end_of, c);
         if (PLAIN || i < s.count) {
-            const float2 e = add2(value(d[i]), r);
-            r = mul2(a[i], e);
-            store_pair<EVEN>(reinterpret_cast<T *>(px), COMP ? mul2(w[i], e) : e, u.mine);
+            const float2 y = add2(value(d[i]), r);
+            r = mul2(a[i], y);
+            store_pair<EVEN>(reinterpret_cast<T *>(px), COMP ? mul2(w[i], y) : y, u.mine);
             store_pair<EVEN>(reinterpret_cast<G *>(pg), mul2(r, x[i]), u.mine);
         }
         px -= p.dx_row;
@@ -724,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
     unsigned char *mine = smem + warp * stages * kBytes;
     Map *maps = reinterpret_cast<Map *>(smem + kWarps * stages * kBytes);
     const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
-    cluster_begin(sh, cluster);
+    cluster_begin(p, sh, cluster);
 
     // steps go from the stream's end
     uint32_t t0 = ((uint32_t)(u.steps - 1) * cluster + u.rank) * kTile + warp * kSpan, ahead = t0;
@@ -769,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
     for (int step = 0, stage = 0; step < u.steps; ++step, t0 -= cluster * kTile, dx -= p.dx_step, dg -= p.dg_step) {
         float2 h = saved(t0);
         const Span s = span_at<kSpan>(p, sh, u, t0, warp, lane, &seq);
+        const Early e = early(p.h0, p, u, __ffs(s.m.starts) - 1, start_of, c), l = early(p.dhT, p, u, 31 - __clz(s.m.ends), end_of, c);
         copy_wait(stages - 1);
         __syncwarp();
         float2 a[kSpan], w[kSpan], x[kSpan];
@@ -799,11 +822,11 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
 #pragma unroll
             for (int i = 0; i < kSpan; ++i) v[i] = COMP ? mul2(w[i], x[i]) : x[i];
             if (s.plain) {
-                f = map_span<true>(p, u, a, v, 0, nullptr, c);
-                Y = map_back<true>(p, u, a, d, s, end_of, c);
+                f = map_span<true>(p, u, a, v, 0, e, nullptr, c);
+                Y = map_back<true>(p, u, a, d, s, l, end_of, c);
             } else {
-                f = map_span<false>(p, u, a, v, s.m.starts, start_of, c);
-                Y = map_back<false>(p, u, a, d, s, end_of, c);
+                f = map_span<false>(p, u, a, v, s.m.starts, e, start_of, c);
+                Y = map_back<false>(p, u, a, d, s, l, end_of, c);
             }
         }
         const bool ends = s.m.ends != 0;
@@ -859,9 +882,9 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const _
         if (sh.dead) break;
         const float2 r = cut ? PY : fma2(PA, sh.enter[lane], PY);
         if (s.plain)
-            run_back<true, COMP, ALIGNED>(p, u, a, w, x, d, h, r, s, start_of, end_of, c, reinterpret_cast<T *>(dx), reinterpret_cast<G *>(dg));
+            run_back<true, COMP, ALIGNED>(p, u, a, w, x, d, h, r, s, e, l, start_of, end_of, c, reinterpret_cast<T *>(dx), reinterpret_cast<G *>(dg));
         else
-            run_back<false, COMP, ALIGNED>(p, u, a, w, x, d, h, r, s, start_of, end_of, c, reinterpret_cast<T *>(dx), reinterpret_cast<G *>(dg));
+            run_back<false, COMP, ALIGNED>(p, u, a, w, x, d, h, r, s, e, l, start_of, end_of, c, reinterpret_cast<T *>(dx), reinterpret_cast<G *>(dg));
     }
     copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
@@ -950,7 +973,7 @@ cudaError_t fit_of(Kernel kernel, int per_sm, Fit *fits, const Fit **out) {
     if (fit.known.load(std::memory_order_acquire)) return cudaSuccess;
     std::lock_guard<std::mutex> lock(mu);
     if (fit.known.load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemSm - kSmemCta));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((kSmemSm - kSmemCta) / 128 * 128));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int k = 1; k <= kMaxCluster && e == cudaSuccess; ++k) {
         cudaLaunchAttribute attr[1];
@@ -960,7 +983,7 @@ cudaError_t fit_of(Kernel kernel, int per_sm, Fit *fits, const Fit **out) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(k);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemSm / per_sm - kSmemCta;
+        cfg.dynamicSmemBytes = (kSmemSm / per_sm - kSmemCta) / 128 * 128;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
