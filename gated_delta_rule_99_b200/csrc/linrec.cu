@@ -11,8 +11,16 @@
 // same channels: the carrying warps send their tile's map to all of them (st.async through
 // distributed shared memory, counted by an mbarrier: a release would wait for the outputs
 // still being stored) and each folds them in order, so each holds the state that enters its
-// tile and the next step.  The data is read from memory once, by
-// cp.async into a ring of tiles that runs ahead of the steps, each warp copying its own rows.
+// tile and the next step.  The data is read from memory once, by cp.async into a ring of tiles
+// that runs ahead of the steps, each warp copying its own rows.
+//
+// Measured on a B200, bf16 inputs and fp32 gates (of the measured copy rate, 6.56 TB/s): 16 x 4096 x
+// 2048 forward 169 us (97%) and backward 334 us (86%); 4 x 4096 x 2048 54 us (75%) and 96 us (74%),
+// where the rows' channels alone do not fill the GPU and the exchanges show; one row of 262144 x 1024
+// 504 us (65%) and 1056 us (54%), where an exchange takes about 2600 cycles of a step of 6000.  bf16
+// gates are bound by the instructions, 22 per element forward and 47 backward: 156 us (79%) and 305 us
+// (67%) at 16 x 4096 x 2048; the write strength 1 - a costs 15 to 20% more.  Three CTAs per SM in the
+// backward, tiles twice as long or 16 warps with one CTA per SM, and one step ahead were slower.
 //
 // A start of a sequence inside a span drops what comes before it by selection (not by a
 // factor of 0), so that no infinity or NaN crosses; padded tokens are zeros (factor
@@ -36,8 +44,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kCh = 64;        // channels per CTA
 constexpr int kSaved = 64;     // tokens between two saved states
 constexpr int kMaxSpan = 16, kMaxStages = 8, kMaxCluster = 16;
-constexpr int kFwdPerSm = 2, kBwdPerSm = 2;  // CTAs per SM that the registers allow
+constexpr int kPerSm = 2;      // CTAs that an SM's registers hold
 constexpr size_t kSmemSm = 227 * 1024;  // of an SM
+constexpr int kSms = 148;
 constexpr int kCuKept = 256;                // offsets of documents that a CTA keeps
 
 // Tokens per warp: 16 in the forward of bf16 inputs; 8 where the tiles are larger, and in the
@@ -564,7 +573,7 @@ __device__ __forceinline__ void run_span(const LinrecParams &p, const Unit &u, c
 
 // ALIGNED: rows start on 16 bytes, and pairs of channels can be stored at once.
 template <int kSpan, typename T, typename G, bool COMP, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, kFwdPerSm) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __grid_constant__ LinrecParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Shared sh;
     constexpr int kTile = kSpan * kWarps;
@@ -734,7 +743,7 @@ __device__ __forceinline__ void run_back(const LinrecParams &p, const Unit &u, c
 }
 
 template <int kSpan, typename T, typename G, bool COMP, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, kBwdPerSm) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Shared sh;
     constexpr int kTile = kSpan * kWarps;
@@ -953,16 +962,17 @@ enum class Pass { kFwd, kBwd, kDecode };
 
 using Kernel = void (*)(LinrecParams);
 
-// Clusters of each size (1 .. 16 CTAs, per_sm of them on an SM) that a device runs at once: they stay
+// Clusters of each size (1 .. 16 CTAs) that a device runs at once: they stay
 // within a group of SMs, so long ones fit less well (two CTAs per SM on a B200: 296 CTAs singly,
 // 264 in clusters of 8, 224 in clusters of 16).  Asked for once per kernel and device, with the
 // attributes that its launches need.
+constexpr int kDevices = 64;
+constexpr size_t kDynamic = (kSmemSm / kPerSm - kSmemCta) / 128 * 128;
 struct Fit {
     std::atomic<int32_t> known{0};
     int16_t clusters[kMaxCluster + 1];
 };
-cudaError_t fit_of(Kernel kernel, int per_sm, Fit *fits, const Fit **out) {
-    constexpr int kDevices = 16;
+cudaError_t fit_of(Kernel kernel, Fit *fits, const Fit **out) {
     static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -973,7 +983,7 @@ cudaError_t fit_of(Kernel kernel, int per_sm, Fit *fits, const Fit **out) {
     if (fit.known.load(std::memory_order_acquire)) return cudaSuccess;
     std::lock_guard<std::mutex> lock(mu);
     if (fit.known.load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((kSmemSm - kSmemCta) / 128 * 128));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDynamic);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int k = 1; k <= kMaxCluster && e == cudaSuccess; ++k) {
         cudaLaunchAttribute attr[1];
@@ -983,7 +993,7 @@ cudaError_t fit_of(Kernel kernel, int per_sm, Fit *fits, const Fit **out) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(k);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = (kSmemSm / per_sm - kSmemCta) / 128 * 128;
+        cfg.dynamicSmemBytes = kDynamic;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
@@ -1012,15 +1022,15 @@ cudaError_t launch_cluster(Kernel kernel, const LinrecParams &p, size_t smem, cu
 
 template <typename T, typename G, bool COMP, bool ALIGNED>
 cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
-    static Fit fits[2][16];
+    static Fit fits[2][kDevices];
     const bool fwd = pass == Pass::kFwd;
-    const int per_sm = fwd ? kFwdPerSm : kBwdPerSm, tile = kWarps * (fwd ? kFwdSpan<T> : kBwdSpan);
+    const int tile = kWarps * (fwd ? kFwdSpan<T> : kBwdSpan);
     const size_t bytes = (size_t)tile * kCh * (fwd ? sizeof(T) + sizeof(G) : 2 * sizeof(T) + sizeof(G));
     const int64_t tiles = (p.rows_per_stream * p.T + tile - 1) / tile, units = p.streams * p.slabs;
     // the longest clusters that can all run at once, and that the stream fills
     const Kernel kernel = fwd ? linrec_fwd_kernel<kFwdSpan<T>, T, G, COMP, ALIGNED> : linrec_bwd_kernel<kBwdSpan, T, G, COMP, ALIGNED>;
     const Fit *fit = nullptr;
-    cudaError_t err = fit_of(kernel, per_sm, fits[fwd ? 0 : 1], &fit);
+    cudaError_t err = fit_of(kernel, fits[fwd ? 0 : 1], &fit);
     if (err != cudaSuccess) return err;
     p.cluster = 1;
     for (int k = 2; k <= kMaxCluster && k <= tiles; ++k)
@@ -1028,7 +1038,7 @@ cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
     // a ring of as many tiles as the shared memory holds, up to the steps there are
     const int64_t steps = (tiles + p.cluster - 1) / p.cluster;
     const size_t maps = p.cluster > 1 ? 2 * p.cluster * sizeof(Map) : 0;
-    int64_t stages = (int64_t)((kSmemSm / per_sm - kSmemCta - maps) / bytes);
+    int64_t stages = (int64_t)((kSmemSm / kPerSm - kSmemCta - maps) / bytes);
     if (stages > kMaxStages) stages = kMaxStages;
     if (stages > steps) stages = steps;
     p.stages = stages < 1 ? 1 : (int32_t)stages;
@@ -1099,11 +1109,19 @@ gdn_status describe(const gdn_linrec_desc *d, LinrecParams *p) {
     p->BT = d->B * d->T;
     p->D = d->D;
     p->N = d->n_seqs > 0 ? d->n_seqs : d->B;
-    // streams: the packed row, a dense row, or as many short dense rows as fill a tile
-    p->rows_per_stream = d->n_seqs > 0 ? 1 : p->T > 0 && p->T < kSaved ? kSaved / p->T : 1;
+    // streams: the packed row, a dense row, or several rows of less than 64 tokens: as many as fill 64,
+    // or as leave every SM two CTAs if that is twice as many (1024 x 16 x 2048 bf16: 78 us forward and
+    // 138 us backward, 155 and 147 us when they only fill 64; 300 x 7 x 1024 with 16 instead of 9:
+    // 14 and 21 us, 16 and 16 us.  Rows of 100 tokens lose, 64 x 100 x 2048: backward 66 us, singly 59 us)
+    p->slabs = (int32_t)((p->D + kCh - 1) / kCh);
+    p->rows_per_stream = 1;
+    if (d->n_seqs == 0 && p->T > 0 && p->T < kSaved) {
+        const int64_t fill = kSaved / p->T, share = p->N * p->slabs / (2 * kSms);
+        const int64_t rows = share >= 2 * fill ? share : fill;
+        p->rows_per_stream = rows > p->N ? p->N : rows;
+    }
     p->streams = d->n_seqs > 0 ? 1 : (p->N + p->rows_per_stream - 1) / p->rows_per_stream;
     p->single = d->n_seqs > 0 ? d->n_seqs == 1 : p->rows_per_stream == 1;
-    p->slabs = (int32_t)((p->D + kCh - 1) / kCh);
     if (p->streams * p->slabs >= kLim / kMaxCluster) return GDN_ERR_INVALID_ARG;
     p->saved = (p->rows_per_stream * p->T + kSaved - 1) / kSaved;
     const int64_t in[] = {d->x_stride, d->g_stride, d->o_stride, d->dx_stride, d->dg_stride};

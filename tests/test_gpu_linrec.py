@@ -98,6 +98,12 @@ def test_thousands_of_documents_of_no_one_or_a_few_tokens():
     run_and_check(draw(1, sum(lengths), 8, N=4000, seed=8), lengths=lengths)
 
 
+@pytest.mark.parametrize("B,T,D", [(700, 3, 2048), (9001, 1, 770), (1301, 63, 190)])
+def test_many_short_rows(B, T, D):
+    """More rows than fill a tile go through one stream, and the last stream has fewer."""
+    run_and_check(draw(B, T, D, seed=B))
+
+
 def test_rows_of_no_token():
     x = torch.zeros(3, 0, 40, device="cuda")
     h0, dhT = torch.randn(3, 40, device="cuda"), torch.randn(3, 40, device="cuda")
