@@ -14,7 +14,9 @@
 //
 // Measured for 4 x 4096 tokens of 16 + 16 heads x 128: bf16 56 us forward and 90 us backward (73% and
 // 69% of the measured copy rate, bound by the instructions: 65% of the issue slots), fp32 90 and
-// 136 us (90%).  With a warp per row and shared memory between the passes: 335 and 560 us.
+// 136 us (90%).  With a warp per row and shared memory between the passes: 335 and 560 us.  With few
+// heads a token's angles and addresses weigh more than its rows (32 angles cost about 75 instructions, a
+// row 250, the step to another token 150): 8 + 2 heads x 64 bf16 23 and 27 us (28% and 36%).
 #include <cmath>
 
 #include "gdn_internal.cuh"
@@ -25,6 +27,7 @@ namespace {
 constexpr int kMaxD = 256, kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kSms = 148, kPerSm = 3, kBwdPerSm = 2;  // blocks of an SM
 constexpr int kSlots = kSms * kPerSm;  // blocks at most, of both tensors
+constexpr int kAngles = 288;           // angles that a warp keeps, those of its tokens
 
 struct QkParams {
     int64_t tokens;
@@ -33,6 +36,7 @@ struct QkParams {
     int32_t whole;              // every lane has both chunks of its units
     int32_t blocks[2];          // blocks of q and of k
     int32_t per[2], parts[2];   // rows (times 32 / lanes) of a warp's item, and items of a token
+    int32_t group[2];           // tokens side by side in a warp, where it has lanes for all their heads
     float c, eps;
     const int32_t *pos;
     const float *inv_freq;
@@ -189,7 +193,8 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 
     }
 }
 
-// A warp's way through its rows: items (a token's heads, or a part of them) and the rows of an item.
+// A warp's way through its rows: items (a token's heads, or a part of them, or a group's) and the rows
+// of an item.  tok: the token, or the group of tokens.
 // row, drow: where this lane's row is, for reading (x, dy) or writing.
 template <typename P>
 struct Way {
@@ -200,13 +205,14 @@ struct Way {
 };
 
 // ---------------------------------------------------------------- the kernel
-// NU units per lane.  VEC: whole chunks are loaded and stored at once.
-template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD>
+// NU units per lane.  VEC: whole chunks are loaded and stored at once.  GROUP: q or k has few heads, so
+// that a warp takes several tokens at once.
+template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD, bool GROUP>
 __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
     // rows on their way: two, but one in the backward of bf16 rows, whose registers a second one spills (90
     // against 95 us for 4 x 4096 tokens of 16 + 16 heads x 128; fp32: 152 against 136 us the other way)
     constexpr int kUnroll = NU > 1 || (BWD && sizeof(T) == 2) ? 1 : 2;
-    __shared__ __align__(16) float2 angles[kWarps][kMaxD / 2 + 8];  // (cos, sin), see angle_at
+    __shared__ __align__(16) float2 angles[kWarps][GROUP ? kAngles : kMaxD / 2 + 8];  // (cos, sin), see angle_at
     __shared__ float sums[BWD ? kWarps : 1][kMaxD];
     __shared__ __align__(16) float weights[kMaxD];
     const int l = threadIdx.x & 31, wi = threadIdx.x >> 5;
@@ -217,9 +223,11 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
     T *out = static_cast<T *>(BWD ? p.dx[which] : p.y[which]);
     const int64_t xs = p.xs[which], ys = p.ys[which], os = BWD ? p.dxs[which] : ys;
     const int its = (H + side - 1) / side, per = p.per[which], parts = p.parts[which];
-    const uint32_t items = (uint32_t)p.tokens * parts, warps = p.blocks[which] * kWarps;
+    const int group = GROUP ? p.group[which] : 1, slot = GROUP ? sub / H : 0, head = GROUP ? sub - slot * H : sub;
+    const uint32_t tokens = (uint32_t)p.tokens, items = GROUP && group > 1 ? (tokens + group - 1) / group : tokens * parts;
+    const uint32_t warps = p.blocks[which] * kWarps;
 
-    const int units = NU * p.lanes + 1;
+    const int units = NU * p.lanes + 1, table = units * V;
     // this lane's units: where their chunks are (-1: nowhere) and whose angles they take
     int at[NU][2], angle[NU];
     float acc[NU][2][V];
@@ -246,33 +254,70 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
             }
         }
     }
-    for (int i = half + l; i < units * V; i += 32) angles[wi][angle_at<V>(units, i / V, i % V)] = make_float2(1.f, 0.f);
+    for (int i = half + l; i < table; i += 32)
+        for (int g = 0; g < group; ++g) angles[wi][g * table + angle_at<V>(units, i / V, i % V)] = make_float2(1.f, 0.f);
+    const float2 *turns = angles[wi] + (GROUP && group > 1 && slot < group ? slot * table : 0);
 
     __syncthreads();
     // whole: every lane has both chunks of its units, and every row of lanes a head
-    const bool whole = VEC && NU == 1 && H % side == 0 && p.whole;
+    const bool whole = VEC && NU == 1 && (GROUP && group > 1 ? H * group == side && tokens % group == 0 : H % side == 0) && p.whole;
     const int64_t step = (int64_t)side * d;
+    const auto offset = [&](const auto &y, int64_t stride) {
+        if (GROUP && group > 1) return (y.tok * group + slot) * stride + (int64_t)head * d;
+        return y.tok * stride + (int64_t)(y.it * side + sub) * d;
+    };
     const auto enter = [&](auto &y, auto base, int64_t stride) {
-        y.tok = y.item / parts;
+        y.tok = parts == 1 ? y.item : y.item / parts;
         y.it = (y.item - y.tok * parts) * per;
         y.end = y.it + per < its ? y.it + per : its;
-        y.row = base + y.tok * stride + (int64_t)(y.it * side + sub) * d;
+        y.row = base + offset(y, stride);
+    };
+    // whether this lane's row is one
+    const auto is_row = [&](const auto &y) {
+        return whole || (GROUP && group > 1 ? slot < group && y.tok * group + slot < tokens : y.it * side + sub < H);
     };
     Chunk<T, V, VEC> rx[kUnroll][NU][2], rd[BWD ? kUnroll : 1][NU][2];
     int32_t pos[kUnroll];
     Way<const T *> ahead = {(uint32_t)(block * kWarps + wi), 0, 0, 0, 0, nullptr, nullptr};
     Way<T *> go = {ahead.item, 0, 0, 0, 0, nullptr, nullptr};
-    const auto enter_ahead = [&]() {
-        if (ahead.item >= items) return;
-        enter(ahead, x, xs);
-        if (BWD) ahead.drow = dy + ahead.tok * ys + (int64_t)(ahead.it * side + sub) * d;
-        ahead.pos = p.pos ? p.pos[ahead.tok] : (int32_t)(ahead.tok % (uint32_t)p.T);
+    // to the next item; with one per token (or group) by a fixed jump
+    const int64_t skip = (int64_t)warps * group, back = its * step;
+    const auto next = [&](auto &y, auto base, int64_t stride) {
+        y.item += warps;
+        if (parts == 1) {
+            y.tok = y.item;
+            y.it = 0;
+            y.row += skip * stride - back;
+        } else if (y.item < items) {
+            enter(y, base, stride);
+        }
     };
+    const int32_t turn_over = p.T ? (int32_t)((uint32_t)skip % (uint32_t)p.T) : 0;
+    const auto find_pos = [&](bool first) {
+        if (ahead.item >= items) return;
+        uint32_t tok = ahead.tok;
+        if (GROUP && group > 1) {  // lane i: the i-th token's
+            tok = tok * group + l % group;
+            if (tok >= tokens) tok = tokens - 1;
+        }
+        if (p.pos) {
+            ahead.pos = p.pos[tok];
+        } else if (first || parts != 1) {
+            ahead.pos = (int32_t)(tok % (uint32_t)p.T);
+        } else {
+            ahead.pos = ahead.pos >= p.T - turn_over ? ahead.pos - (p.T - turn_over) : ahead.pos + turn_over;
+        }
+    };
+    if (ahead.item < items) {
+        enter(ahead, x, xs);
+        if (BWD) ahead.drow = dy + offset(ahead, ys);
+        find_pos(true);
+    }
     // loads the row that `ahead` is at, and moves on
     const auto load = [&](int u) {
         if (ahead.item >= items) return;
         pos[u] = ahead.pos;
-        const bool in = whole || ahead.it * side + sub < H;
+        const bool in = is_row(ahead);
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
@@ -293,12 +338,12 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
         ahead.row += step;
         if (BWD) ahead.drow += step;
         if (++ahead.it == ahead.end) {
-            ahead.item += warps;
-            enter_ahead();
+            next(ahead, x, xs);
+            if (BWD) ahead.drow = parts == 1 ? ahead.drow + (skip * ys - back) : dy + offset(ahead, ys);
+            find_pos(false);
         }
     };
 
-    enter_ahead();
     if (go.item < items) enter(go, out, os);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) load(u);
@@ -310,11 +355,21 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
             if (angles_of != go.tok) {
                 angles_of = go.tok;
                 __syncwarp();
-                for (int i = l; i < half; i += 32) {
-                    const double t = (double)pos[u] * ((double)p.inv_freq[i] * 0.15915494309189533577);
+                const auto form = [&](int i, int32_t at_pos, float2 *to) {
+                    const double t = (double)at_pos * ((double)p.inv_freq[i] * 0.15915494309189533577);
                     float2 cs;
                     sincospif(2.f * (float)(t - rint(t)), &cs.y, &cs.x);
-                    angles[wi][angle_at<V>(units, i / V, i % V)] = cs;
+                    to[angle_at<V>(units, i / V, i % V)] = cs;
+                };
+                if (GROUP && group > 1) {
+                    int i = l, g = 0;  // angle i of token g
+                    for (int first = 0; first < half * group; first += 32, i += 32) {
+                        while (i >= half) i -= half, ++g;
+                        const int32_t at_pos = __shfl_sync(0xffffffffu, pos[u], g);
+                        if (g < group) form(i, at_pos, angles[wi] + g * table);
+                    }
+                } else {
+                    for (int i = l; i < half; i += 32) form(i, pos[u], angles[wi]);
                 }
                 __syncwarp();
             }
@@ -329,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                     for (int i = 0; i < V; ++i) s = fmaf(a[k][e][i], a[k][e][i], s);
                 }
                 if (BWD) {
-                    turn<V, ADJ, true>(g[k][0], g[k][1], angles[wi] + angle_at<V>(units, angle[k], 0), units);
+                    turn<V, ADJ, true>(g[k][0], g[k][1], turns + angle_at<V>(units, angle[k], 0), units);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float w[V];
@@ -345,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
             }
             const float r = scale_of(p, s);
             const float cd = p.norm == GDN_NORM_NONE ? 0.f : p.c * (r * dot);
-            const bool in = whole || go.it * side + sub < H;
+            const bool in = is_row(go);
 #pragma unroll
             for (int k = 0; k < NU; ++k) {
 #pragma unroll
@@ -363,17 +418,14 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                         }
                     }
                 }
-                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], angles[wi] + angle_at<V>(units, angle[k], 0), units);
+                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], turns + angle_at<V>(units, angle[k], 0), units);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     if (whole || (in && at[k][e] >= 0)) Chunk<T, V, VEC>::store(go.row + at[k][e], a[k][e]);
             }
             load(u);
             go.row += step;
-            if (++go.it == go.end) {
-                go.item += warps;
-                if (go.item < items) enter(go, out, os);
-            }
+            if (++go.it == go.end) next(go, out, os);
         }
     }
     if (BWD && p.dw[which]) {
@@ -425,18 +477,32 @@ cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
     p.lanes = 1 << p.lanes_log2;
     p.whole = NU == 1 && p.lanes * 2 * V == p.d;
     const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? kBwdPerSm : kPerSm);
-    // a warp takes all heads of a token, or fewer where that leaves warps without work
-    int64_t rows[2], blocks[2];
-    for (int i = 0; i < 2; ++i) rows[i] = (p.heads[i] + side - 1) / side;
+    // a warp takes all heads of a token, or fewer where that leaves warps without work, or several tokens
+    // where their heads fit its lanes and every warp has some.  16384 tokens, bf16, without and with: 4 + 4
+    // heads x 64 forward 23.3 and 20.5 us, backward 30.1 and 23.0 us; 8 + 2 x 64 backward 29.8 and 26.6 us.
+    // The forward does so for both tensors or none (8 + 1 x 128: 30.5 us, 32.9 us with k alone)
+    int64_t rows[2], items[2], blocks[2];
     for (int i = 0; i < 2; ++i) {
-        const int64_t fair = p.tokens * (rows[0] + rows[1]) / (most * kWarps);  // rows per warp if all had some
+        rows[i] = (p.heads[i] + side - 1) / side;
+        p.group[i] = 1;
+        if (NU == 1 && p.tokens >= 2 * most * kWarps)
+            while ((p.group[i] + 1) * p.heads[i] <= side && (p.group[i] + 1) * (p.lanes + 1) * V <= kAngles) ++p.group[i];
+    }
+    if (!bwd && (p.group[0] == 1 || p.group[1] == 1)) p.group[0] = p.group[1] = 1;
+    for (int i = 0; i < 2; ++i) items[i] = (p.tokens + p.group[i] - 1) / p.group[i];
+    const int64_t fair = (items[0] * rows[0] + items[1] * rows[1]) / (most * kWarps);  // rows per warp if all had some
+    for (int i = 0; i < 2; ++i) {
         p.per[i] = (int32_t)(fair < 1 ? 1 : fair < rows[i] ? fair : rows[i]);
         p.parts[i] = (int32_t)((rows[i] + p.per[i] - 1) / p.per[i]);
-        blocks[i] = (p.tokens * p.parts[i] + kWarps - 1) / kWarps;
+        blocks[i] = (items[i] * p.parts[i] + kWarps - 1) / kWarps;
         if (blocks[i] < 1) blocks[i] = 1;
     }
-    if (blocks[0] + blocks[1] > most) {  // share them out by the work, and walk
-        int64_t q = most * rows[0] / (rows[0] + rows[1]);
+    if (blocks[0] + blocks[1] > most) {
+        // walk, with shares by the instructions: about 250 for a row (backward 430), 100 for an item and 60
+        // for every 32 angles
+        int64_t work[2];
+        for (int i = 0; i < 2; ++i) work[i] = items[i] * (rows[i] * (bwd ? 14 : 8) + 3 + 2 * ((half * p.group[i] + 31) / 32));
+        int64_t q = most * work[0] / (work[0] + work[1]);
         q = q < 1 ? 1 : q > most - 1 ? most - 1 : q;
         if (q < blocks[0]) blocks[0] = q;
         if (most - q < blocks[1]) blocks[1] = most - q;
@@ -444,12 +510,19 @@ cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
     p.blocks[0] = (int32_t)blocks[0];
     p.blocks[1] = (int32_t)blocks[1];
     const unsigned grid = (unsigned)(blocks[0] + blocks[1]);
+    constexpr bool kGroups = NU == 1;
+    const bool group = kGroups && (p.group[0] > 1 || p.group[1] > 1);
     if (!bwd) {
-        if (p.tokens) GDN_LAUNCH(kKQkRope, s, qk_kernel<T, V, NU, VEC, ADJ, false><<<grid, kThreads, 0, s>>>(p));
+        if (p.tokens && group)
+            GDN_LAUNCH(kKQkRope, s, qk_kernel<T, V, NU, VEC, ADJ, false, kGroups><<<grid, kThreads, 0, s>>>(p));
+        else if (p.tokens)
+            GDN_LAUNCH(kKQkRope, s, qk_kernel<T, V, NU, VEC, ADJ, false, false><<<grid, kThreads, 0, s>>>(p));
         return cudaSuccess;
     }
-    if (p.tokens || p.dw[0] || p.dw[1])
-        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, V, NU, VEC, ADJ, true><<<grid, kThreads, 0, s>>>(p));
+    if (group)
+        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, V, NU, VEC, ADJ, true, kGroups><<<grid, kThreads, 0, s>>>(p));
+    else if (p.tokens || p.dw[0] || p.dw[1])
+        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, V, NU, VEC, ADJ, true, false><<<grid, kThreads, 0, s>>>(p));
     if (p.dw[0] || p.dw[1])
         GDN_LAUNCH(kKQkRopeDw, s, qk_dw_kernel<<<dim3((p.d + 31) / 32, 2), dim3(32, 32), 0, s>>>(p));
     return cudaSuccess;

@@ -208,7 +208,7 @@ gdn_status gdn_decode(const gdn_desc *desc, const void *q, const void *k, const 
  *
  * g is the log-decay, one value per token and channel (g <= 0 in use; -inf is
  * a reset to w_t x_t; a positive g grows the state, and the products of the
- * factors over up to 64 tokens then have to stay below the fp32 maximum).
+ * factors over up to 128 tokens then have to stay below the fp32 maximum).
  * A NaN or infinity stays in its channel and its sequence.
  *
  * Layouts: x, o, do_, dx [B][T][D] in dtype; g, dg [B][T][D] in g_dtype

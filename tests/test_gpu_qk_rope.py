@@ -87,6 +87,26 @@ def test_token_and_head_counts(B, T, Hq, Hk, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hk,d,rot,interleaved", [(8, 2, 64, 64, False), (3, 1, 64, 32, True), (5, 3, 32, 8, True),
+                                                     (1, 1, 16, 0, False), (2, 1, 128, 48, False), (1, 1, 24, 24, True),
+                                                     (2, 1, 256, 256, False), (1, 7, 8, 8, True)])
+def test_few_heads_of_many_tokens(Hq, Hk, d, rot, interleaved, dtype):
+    """A warp takes several tokens at once, fewer at the end; in column slices of one projection too."""
+    v = draw(3, 2501, Hq, Hk, d, rot, dtype, seed=d + rot, far=100000)
+    want = run_and_check(v, interleaved=interleaved)
+    v["positions"] = None
+    run_and_check(v, "l2", interleaved=interleaved)
+    v["positions"] = draw(3, 2501, Hq, Hk, d, rot, dtype, seed=d + rot, far=100000)["positions"]
+
+    def sliced(t):
+        wide = torch.full(t.shape[:2] + (t.shape[2] + 2, d), float("nan"), dtype=t.dtype, device="cuda")
+        wide[:, :, 1:-1] = t.cuda()
+        return wide[:, :, 1:-1]
+    for one, two in zip(want, run_and_check(v, interleaved=interleaved, on=sliced)):
+        assert torch.equal(one, two)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_far_and_negative_positions(dtype):
     v = draw(2, 40, 2, 2, 128, 128, dtype, far=1 << 20)
     v["positions"][0, :4] = torch.tensor([2 ** 31 - 1, -2 ** 31, 0, 1 << 24])
