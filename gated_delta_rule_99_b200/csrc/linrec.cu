@@ -450,9 +450,12 @@ __device__ __forceinline__ void cluster_begin(const LinrecParams &p, Shared &sh,
 __device__ __forceinline__ void cluster_ready(int cluster) {
     if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// No CTA leaves while another may still send to it.
-__device__ __forceinline__ void cluster_end(int cluster) {
+// No CTA leaves while another may still send to it.  One that gave up has not seen all maps arrive: half a
+// millisecond for those on their way, to it or from it.
+__device__ __forceinline__ void cluster_end(const Shared &sh, int cluster) {
     if (cluster > 1) {
+        if (sh.dead)
+            for (int i = 0; i < 512; ++i) __nanosleep(1000);
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     }
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __gr
     }
     copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
-    cluster_end(cluster);
+    cluster_end(sh, cluster);
 }
 
 // ---------------------------------------------------------------- backward
@@ -897,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __gr
     }
     copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
-    cluster_end(cluster);
+    cluster_end(sh, cluster);
 }
 
 // ---------------------------------------------------------------- one-token form
