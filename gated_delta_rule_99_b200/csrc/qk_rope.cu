@@ -155,17 +155,88 @@ __device__ __forceinline__ void weights_of(const float *from, int n, int j, int 
     }
 }
 
-// Where angle i of unit j is among a warp's: pairs of angles of neighbouring units side by side, so
-// that a row's lanes read adjacent 16 bytes.  n: units and one for what is not turned.
+// Two values per instruction where V is even: d = a b + c, and a b.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <int V>
+__device__ __forceinline__ void fma_into(float (&c)[V], const float (&a)[V], const float (&b)[V]) {
+    if (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const int j = (i + 1) % V;
+            const float2 t = __ffma2_rn(make_float2(a[i], a[j]), make_float2(b[i], b[j]), make_float2(c[i], c[j]));
+            c[i] = t.x, c[j] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = fmaf(a[i], b[i], c[i]);
+    }
+}
+// The same summed into s.
+template <int V>
+__device__ __forceinline__ void dot_into(float2 &s, const float (&a)[V], const float (&b)[V]) {
+    if (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) s = __ffma2_rn(make_float2(a[i], a[(i + 1) % V]), make_float2(b[i], b[(i + 1) % V]), s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s.x = fmaf(a[i], b[i], s.x);
+    }
+}
+template <int V>
+__device__ __forceinline__ void times(float (&a)[V], const float (&b)[V]) {
+    if (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const int j = (i + 1) % V;
+            const float2 t = __fmul2_rn(make_float2(a[i], a[j]), make_float2(b[i], b[j]));
+            a[i] = t.x, a[j] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] *= b[i];
+    }
+}
+template <int V>
+__device__ __forceinline__ void times(float (&a)[V], float r) {
+    float b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = r;
+    times<V>(a, b);
+}
+
+// A warp's angles: pairs of a unit's angles side by side and neighbouring units next to each other, so
+// that a row's lanes read adjacent 16 bytes: two cosines and two sines (adjacent pairs: cosine and
+// sine of each).  n: units and one for what is not turned.
 template <int V>
 __device__ __forceinline__ int angle_at(int n, int j, int i) {
     return V % 2 ? n * i + j : 2 * (n * (i / 2) + j) + i % 2;
 }
+template <int V, bool ADJ>
+__device__ __forceinline__ void put_angle(float2 *angles, int n, int j, int i, float2 cs) {
+    if (V % 2 || ADJ) {
+        angles[angle_at<V>(n, j, i)] = cs;
+    } else {
+        float *to = reinterpret_cast<float *>(angles + angle_at<V>(n, j, i - i % 2)) + i % 2;
+        to[0] = cs.x, to[2] = cs.y;
+    }
+}
 
-// A pair of chunks turned by the angles whose (cos, sin) are given (BACK: turned back).  Adjacent
-// pairs: the first V / 2 angles are the first chunk's.
+// A pair of chunks turned by a unit's angles (BACK: turned back).  Adjacent pairs: the first V / 2
+// angles are the first chunk's.
 template <int V, bool ADJ, bool BACK>
 __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *angles, int n) {
+    if (V % 2 == 0 && !ADJ) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const int f = (e + 1) % V;
+            const float4 t = *reinterpret_cast<const float4 *>(angles + angle_at<V>(n, 0, e));
+            const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w);
+            const float2 u = make_float2(a[e], a[f]), v = make_float2(b[e], b[f]), m = __fmul2_rn(BACK ? u : v, both(-1.f));
+            const float2 x = __ffma2_rn(u, c, __fmul2_rn(BACK ? v : m, s)), y = __ffma2_rn(v, c, __fmul2_rn(BACK ? m : u, s));
+            a[e] = x.x, a[f] = x.y, b[e] = y.x, b[f] = y.y;
+        }
+        return;
+    }
     float2 cs[V];
     if (V % 2 == 0) {  // two angles per load
 #pragma unroll
@@ -255,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
         }
     }
     for (int i = half + l; i < table; i += 32)
-        for (int g = 0; g < group; ++g) angles[wi][g * table + angle_at<V>(units, i / V, i % V)] = make_float2(1.f, 0.f);
+        for (int g = 0; g < group; ++g) put_angle<V, ADJ>(angles[wi] + g * table, units, i / V, i % V, make_float2(1.f, 0.f));
     const float2 *turns = angles[wi] + (GROUP && group > 1 && slot < group ? slot * table : 0);
 
     __syncthreads();
@@ -359,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                     const double t = (double)at_pos * ((double)p.inv_freq[i] * 0.15915494309189533577);
                     float2 cs;
                     sincospif(2.f * (float)(t - rint(t)), &cs.y, &cs.x);
-                    to[angle_at<V>(units, i / V, i % V)] = cs;
+                    put_angle<V, ADJ>(to, units, i / V, i % V, cs);
                 };
                 if (GROUP && group > 1) {
                     int i = l, g = 0;  // angle i of token g
@@ -373,15 +444,15 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                 }
                 __syncwarp();
             }
-            float a[NU][2][V], g[NU][2][V], s = 0.f, dot = 0.f;
+            float a[NU][2][V], g[NU][2][V];
+            float2 s2 = both(0.f), dot2 = both(0.f);
 #pragma unroll
             for (int k = 0; k < NU; ++k) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     rx[u][k][e].get(a[k][e]);
                     if (BWD) rd[u][k][e].get(g[k][e]);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) s = fmaf(a[k][e][i], a[k][e][i], s);
+                    dot_into<V>(s2, a[k][e], a[k][e]);
                 }
                 if (BWD) {
                     turn<V, ADJ, true>(g[k][0], g[k][1], turns + angle_at<V>(units, angle[k], 0), units);
@@ -389,11 +460,12 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                     for (int e = 0; e < 2; ++e) {
                         float w[V];
                         weights_of<V>(weights, units - 1, unit + k * p.lanes, e, w);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) dot = fmaf(g[k][e][i] * w[i], a[k][e][i], dot);
+                        times<V>(w, g[k][e]);
+                        dot_into<V>(dot2, w, a[k][e]);
                     }
                 }
             }
+            float s = s2.x + s2.y, dot = dot2.x + dot2.y;
             for (int off = p.lanes >> 1; off > 0; off >>= 1) {
                 s += __shfl_xor_sync(0xffffffffu, s, off);
                 if (BWD) dot += __shfl_xor_sync(0xffffffffu, dot, off);
@@ -407,15 +479,19 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                 for (int e = 0; e < 2; ++e) {
                     float w[V];
                     weights_of<V>(weights, units - 1, unit + k * p.lanes, e, w);
+                    times<V>(a[k][e], r);
+                    if (BWD) {
+                        float cds[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xn = a[k][e][i] * r;
-                        if (BWD) {
-                            acc[k][e][i] = fmaf(g[k][e][i], xn, acc[k][e][i]);
-                            a[k][e][i] = r * fmaf(-xn, cd, g[k][e][i] * w[i]);
-                        } else {
-                            a[k][e][i] = xn * w[i];
-                        }
+                        for (int i = 0; i < V; ++i) cds[i] = -cd;
+                        fma_into<V>(acc[k][e], g[k][e], a[k][e]);
+                        times<V>(w, g[k][e]);
+                        fma_into<V>(w, a[k][e], cds);
+                        times<V>(w, r);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) a[k][e][i] = w[i];
+                    } else {
+                        times<V>(a[k][e], w);
                     }
                 }
                 if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], turns + angle_at<V>(units, angle[k], 0), units);
