@@ -280,9 +280,9 @@ struct Way {
 // that a warp takes several tokens at once.
 template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD, bool GROUP>
 __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
-    // rows on their way: two, but one in the backward of bf16 rows, whose registers a second one spills (90
-    // against 95 us for 4 x 4096 tokens of 16 + 16 heads x 128; fp32: 152 against 136 us the other way)
-    constexpr int kUnroll = NU > 1 || (BWD && sizeof(T) == 2) ? 1 : 2;
+    // rows on their way while a warp works on one: one, but two in the backward of fp32 rows (4 x 4096 tokens of
+    // 16 + 16 heads x 128: 134 against 139 us), whose bytes are twice as many
+    constexpr int kUnroll = BWD && sizeof(T) == 4 && NU == 1 && !GROUP ? 2 : 1;
     __shared__ __align__(16) float2 angles[kWarps][GROUP ? kAngles : kMaxD / 2 + 8];  // (cos, sin), see angle_at
     __shared__ float sums[BWD ? kWarps : 1][kMaxD];
     __shared__ __align__(16) float weights[kMaxD];
@@ -446,14 +446,19 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
             }
             float a[NU][2][V], g[NU][2][V];
             float2 s2 = both(0.f), dot2 = both(0.f);
+            const bool in = is_row(go);
 #pragma unroll
-            for (int k = 0; k < NU; ++k) {
+            for (int k = 0; k < NU; ++k)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     rx[u][k][e].get(a[k][e]);
                     if (BWD) rd[u][k][e].get(g[k][e]);
-                    dot_into<V>(s2, a[k][e], a[k][e]);
                 }
+            if (kUnroll == 1) load(u);  // at once, so that it overlaps the row's arithmetic
+#pragma unroll
+            for (int k = 0; k < NU; ++k) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) dot_into<V>(s2, a[k][e], a[k][e]);
                 if (BWD) {
                     turn<V, ADJ, true>(g[k][0], g[k][1], turns + angle_at<V>(units, angle[k], 0), units);
 #pragma unroll
@@ -465,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                     }
                 }
             }
+            if (kUnroll > 1) load(u);
             float s = s2.x + s2.y, dot = dot2.x + dot2.y;
             for (int off = p.lanes >> 1; off > 0; off >>= 1) {
                 s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -472,7 +478,6 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
             }
             const float r = scale_of(p, s);
             const float cd = p.norm == GDN_NORM_NONE ? 0.f : p.c * (r * dot);
-            const bool in = is_row(go);
 #pragma unroll
             for (int k = 0; k < NU; ++k) {
 #pragma unroll
@@ -499,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                 for (int e = 0; e < 2; ++e)
                     if (whole || (in && at[k][e] >= 0)) Chunk<T, V, VEC>::store(go.row + at[k][e], a[k][e]);
             }
-            load(u);
             go.row += step;
             if (++go.it == go.end) next(go, out, os);
         }
