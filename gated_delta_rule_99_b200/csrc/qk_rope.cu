@@ -12,11 +12,12 @@
 // weights' gradients are summed in registers over a block's rows, written once per block, and
 // added in block order by a second kernel.
 //
-// Measured for 4 x 4096 tokens of 16 + 16 heads x 128: bf16 56 us forward and 90 us backward (73% and
-// 69% of the measured copy rate, bound by the instructions: 65% of the issue slots), fp32 90 and
-// 136 us (90%).  With a warp per row and shared memory between the passes: 335 and 560 us.  With few
-// heads a token's angles and addresses weigh more than its rows (32 angles cost about 75 instructions, a
-// row 250, the step to another token 150): 8 + 2 heads x 64 bf16 23 and 27 us (28% and 36%).
+// Measured for 4 x 4096 tokens of 16 + 16 heads x 128: bf16 52 us forward and 77 us backward (78% and
+// 79% of the measured copy rate), fp32 88 and 133 us (93% and 92%).  With a warp per row and shared
+// memory between the passes: 335 and 560 us; with a row's loads behind the one before it 56 and 90 us.
+// With few heads a token's angles and addresses weigh more than its rows (32 angles cost about 75
+// instructions, a row 250, the step to another token 150): 8 + 2 heads x 64 bf16 20 and 24 us (31% and
+// 40%).  Three blocks per SM in the forward: 53 us, fp32 92 us; with 8 + 1 heads 27 us, four 28 us.
 #include <cmath>
 
 #include "gdn_internal.cuh"
@@ -25,7 +26,7 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxD = 256, kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSms = 148, kPerSm = 3, kBwdPerSm = 2;  // blocks of an SM
+constexpr int kSms = 148, kPerSm = 4, kBwdPerSm = 2;  // blocks of an SM
 constexpr int kSlots = kSms * kPerSm;  // blocks at most, of both tensors
 constexpr int kAngles = 288;           // angles that a warp keeps, those of its tokens
 
@@ -559,8 +560,8 @@ cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
     const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? kBwdPerSm : kPerSm);
     // a warp takes all heads of a token, or fewer where that leaves warps without work, or several tokens
     // where their heads fit its lanes and every warp has some.  16384 tokens, bf16, without and with: 4 + 4
-    // heads x 64 forward 23.3 and 20.5 us, backward 30.1 and 23.0 us; 8 + 2 x 64 backward 29.8 and 26.6 us.
-    // The forward does so for both tensors or none (8 + 1 x 128: 30.5 us, 32.9 us with k alone)
+    // heads x 64 forward 20.5 and 18.3 us, backward 28.1 and 22.0 us; 8 + 2 x 64 backward 28.1 and 24.5 us.
+    // The forward does so for both tensors or none (8 + 1 x 128: 27.1 us, 29.2 us with k alone)
     int64_t rows[2], items[2], blocks[2];
     for (int i = 0; i < 2; ++i) {
         rows[i] = (p.heads[i] + side - 1) / side;
