@@ -6,7 +6,7 @@
 // where pairs are adjacent or nothing turns.  A lane holds one unit, so norm and rotation
 // need no exchange but the sum of squares over the row's lanes (8 lanes of a bf16 row of
 // 128), and 32 / lanes heads of a token run side by side in a warp.  A warp walks the heads
-// of its tokens with a ring of loads kUnroll rows deep; the angles of a token are formed
+// of its tokens, asking for the next row before it works on one; the angles of a token are formed
 // once per warp (64-bit product and reduction, sincospi of the fraction) and shared through
 // shared memory by all its heads.  Bound by HBM: every row is read and written once.  The
 // weights' gradients are summed in registers over a block's rows, written once per block, and
@@ -26,7 +26,9 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxD = 256, kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSms = 148, kPerSm = 4, kBwdPerSm = 2;  // blocks of an SM
+// Blocks of an SM.  Rows that are turned in part take more registers (56 us forward and 80 us backward for
+// half of 4 x 4096 x 32 rows of 128 bf16; with four blocks 62 us).
+constexpr int kSms = 148, kPerSm = 4, kPartPerSm = 3, kBwdPerSm = 2;
 constexpr int kSlots = kSms * kPerSm;  // blocks at most, of both tensors
 constexpr int kAngles = 288;           // angles that a warp keeps, those of its tokens
 
@@ -222,10 +224,12 @@ __device__ __forceinline__ void put_angle(float2 *angles, int n, int j, int i, f
     }
 }
 
-// A pair of chunks turned by a unit's angles (BACK: turned back).  Adjacent pairs: the first V / 2
+// A pair of chunks turned by the first `some` of a unit's angles (BACK: turned back; halves: by all or
+// none).  The others are not even turned by 0, so that no infinity crosses.  Adjacent pairs: the first V / 2
 // angles are the first chunk's.
 template <int V, bool ADJ, bool BACK>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *angles, int n) {
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *angles, int n, int some) {
+    if (some <= 0) return;
     if (V % 2 == 0 && !ADJ) {
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
@@ -259,8 +263,8 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 
             float(&t)[V] = e < V / 2 ? a : b;
             const int i = 2 * (e % (V / 2 ? V / 2 : 1));
             const float u = t[i], v = t[(i + 1) % V];
-            t[i] = fmaf(u, c, -v * sn);
-            t[(i + 1) % V] = fmaf(u, sn, v * c);
+            t[i] = e < some ? fmaf(u, c, -v * sn) : u;
+            t[(i + 1) % V] = e < some ? fmaf(u, sn, v * c) : v;
         }
     }
 }
@@ -278,9 +282,9 @@ struct Way {
 
 // ---------------------------------------------------------------- the kernel
 // NU units per lane.  VEC: whole chunks are loaded and stored at once.  GROUP: q or k has few heads, so
-// that a warp takes several tokens at once.
-template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD, bool GROUP>
-__global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(const __grid_constant__ QkParams p) {
+// that a warp takes several tokens at once.  FULL: whole rows are turned.
+template <typename T, int V, int NU, bool VEC, bool ADJ, bool BWD, bool GROUP, bool FULL>
+__global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : FULL ? kPerSm : kPartPerSm) qk_kernel(const __grid_constant__ QkParams p) {
     // rows on their way while a warp works on one: one, but two in the backward of fp32 rows (4 x 4096 tokens of
     // 16 + 16 heads x 128: 134 against 139 us), whose bytes are twice as many
     constexpr int kUnroll = BWD && sizeof(T) == 4 && NU == 1 && !GROUP ? 2 : 1;
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
 #pragma unroll
                 for (int e = 0; e < 2; ++e) dot_into<V>(s2, a[k][e], a[k][e]);
                 if (BWD) {
-                    turn<V, ADJ, true>(g[k][0], g[k][1], turns + angle_at<V>(units, angle[k], 0), units);
+                    turn<V, ADJ, true>(g[k][0], g[k][1], turns + angle_at<V>(units, angle[k], 0), units, FULL ? V : half - angle[k] * V);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float w[V];
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                         for (int i = 0; i < V; ++i) cds[i] = -cd;
                         fma_into<V>(acc[k][e], g[k][e], a[k][e]);
                         times<V>(w, g[k][e]);
-                        fma_into<V>(w, a[k][e], cds);
+                        if (p.norm != GDN_NORM_NONE) fma_into<V>(w, a[k][e], cds);
                         times<V>(w, r);
 #pragma unroll
                         for (int i = 0; i < V; ++i) a[k][e][i] = w[i];
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdPerSm : kPerSm) qk_kernel(
                         times<V>(a[k][e], w);
                     }
                 }
-                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], turns + angle_at<V>(units, angle[k], 0), units);
+                if (!BWD) turn<V, ADJ, false>(a[k][0], a[k][1], turns + angle_at<V>(units, angle[k], 0), units, FULL ? V : half - angle[k] * V);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     if (whole || (in && at[k][e] >= 0)) Chunk<T, V, VEC>::store(go.row + at[k][e], a[k][e]);
@@ -551,13 +555,14 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const __grid_constant__ QkP
 // ---------------------------------------------------------------- launches
 template <typename T, int V, int NU, bool VEC, bool ADJ>
 cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
+    const bool full = NU == 1 && p.rot == p.d;
     // lanes of a row: a power of two that its units fit
     const int half = p.rot / 2, units = ADJ ? (p.d + 2 * V - 1) / (2 * V) : half / V + (p.d - p.rot + 2 * V - 1) / (2 * V);
     p.lanes_log2 = 0;
     while ((1 << p.lanes_log2) < (units + NU - 1) / NU) ++p.lanes_log2;
     p.lanes = 1 << p.lanes_log2;
     p.whole = NU == 1 && p.lanes * 2 * V == p.d;
-    const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? kBwdPerSm : kPerSm);
+    const int side = 32 >> p.lanes_log2, most = kSms * (bwd ? kBwdPerSm : full ? kPerSm : kPartPerSm);
     // a warp takes all heads of a token, or fewer where that leaves warps without work, or several tokens
     // where their heads fit its lanes and every warp has some.  16384 tokens, bf16, without and with: 4 + 4
     // heads x 64 forward 20.5 and 18.3 us, backward 28.1 and 22.0 us; 8 + 2 x 64 backward 28.1 and 24.5 us.
@@ -591,19 +596,22 @@ cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
     p.blocks[0] = (int32_t)blocks[0];
     p.blocks[1] = (int32_t)blocks[1];
     const unsigned grid = (unsigned)(blocks[0] + blocks[1]);
-    constexpr bool kGroups = NU == 1;
-    const bool group = kGroups && (p.group[0] > 1 || p.group[1] > 1);
+    constexpr bool kVariants = NU == 1;
+    const bool group = kVariants && (p.group[0] > 1 || p.group[1] > 1);
+    using Kernel = void (*)(QkParams);
+    const Kernel kernel = !bwd ? !group ? full ? qk_kernel<T, V, NU, VEC, ADJ, false, false, kVariants>
+                                               : qk_kernel<T, V, NU, VEC, ADJ, false, false, false>
+                                        : full ? qk_kernel<T, V, NU, VEC, ADJ, false, kVariants, kVariants>
+                                               : qk_kernel<T, V, NU, VEC, ADJ, false, kVariants, false>
+                               : !group ? full ? qk_kernel<T, V, NU, VEC, ADJ, true, false, kVariants>
+                                               : qk_kernel<T, V, NU, VEC, ADJ, true, false, false>
+                                        : full ? qk_kernel<T, V, NU, VEC, ADJ, true, kVariants, kVariants>
+                                               : qk_kernel<T, V, NU, VEC, ADJ, true, kVariants, false>;
     if (!bwd) {
-        if (p.tokens && group)
-            GDN_LAUNCH(kKQkRope, s, qk_kernel<T, V, NU, VEC, ADJ, false, kGroups><<<grid, kThreads, 0, s>>>(p));
-        else if (p.tokens)
-            GDN_LAUNCH(kKQkRope, s, qk_kernel<T, V, NU, VEC, ADJ, false, false><<<grid, kThreads, 0, s>>>(p));
+        if (p.tokens) GDN_LAUNCH(kKQkRope, s, kernel<<<grid, kThreads, 0, s>>>(p));
         return cudaSuccess;
     }
-    if (group)
-        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, V, NU, VEC, ADJ, true, kGroups><<<grid, kThreads, 0, s>>>(p));
-    else if (p.tokens || p.dw[0] || p.dw[1])
-        GDN_LAUNCH(kKQkRopeBwd, s, qk_kernel<T, V, NU, VEC, ADJ, true, false><<<grid, kThreads, 0, s>>>(p));
+    if (p.tokens || p.dw[0] || p.dw[1]) GDN_LAUNCH(kKQkRopeBwd, s, kernel<<<grid, kThreads, 0, s>>>(p));
     if (p.dw[0] || p.dw[1])
         GDN_LAUNCH(kKQkRopeDw, s, qk_dw_kernel<<<dim3((p.d + 31) / 32, 2), dim3(32, 32), 0, s>>>(p));
     return cudaSuccess;

@@ -114,6 +114,31 @@ def test_far_and_negative_positions(dtype):
         run_and_check(v, interleaved=interleaved)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 32), (64, 24), (10, 6), (128, 0), (80, 72)])
+def test_non_finite_values_that_are_not_turned_stay_where_they_are(d, rot, interleaved, dtype):
+    """Without a norm a value behind the rotated ones touches no other, and no gradient but its weight's."""
+    v = draw(2, 6, 3, 2, d, rot, dtype, seed=d + rot)
+    dev = {n: None if t is None else t.cuda() for n, t in v.items()}
+    kw = dict(inv_freq=dev["inv_freq"] if rot else None, norm=None, q_weight=dev["q_weight"],
+              k_weight=dev["k_weight"], interleaved=interleaved)
+    fwd = lambda: gdn.gdn_qk_norm_rope_fwd(dev["q"], dev["k"], **kw)
+    bwd = lambda: gdn.gdn_qk_norm_rope_bwd(dev["q"], dev["k"], dev["dqo"], dev["dko"], **kw)
+    q, k = fwd()
+    grads = bwd()
+    hit = torch.zeros(v["q"].shape, dtype=torch.bool, device="cuda")
+    for i, bad in enumerate((float("inf"), -float("inf"), float("nan"))):
+        for at in range(rot + i, d, 3):
+            dev["q"][i % 2, i, (at + i) % 3, at] = bad
+            hit[i % 2, i, (at + i) % 3, at] = True
+    q2, k2 = fwd()
+    assert torch.equal(q2[~hit], q[~hit]) and not torch.isfinite(q2[hit]).any() and torch.equal(k2, k)
+    dq, dk, dqw, dkw = bwd()
+    assert torch.equal(dq, grads[0]) and torch.equal(dk, grads[1]) and torch.equal(dkw, grads[3])
+    assert torch.equal(dqw[:rot], grads[2][:rot])
+
+
 def test_one_weight_only_and_given_eps():
     v = draw(2, 9, 3, 2, 64, 64, "fp32")
     v["q_weight"] = None
