@@ -1,4 +1,5 @@
-"""B200-native (sm_100a) chunkwise Gated DeltaNet layer, forward and backward.
+"""B200-native (sm_100a) chunkwise Gated DeltaNet layer, forward and backward, and two
+operators around it: the gated linear recurrence and the q/k normalisation with rotation.
 
 The compute lives in libgdn.so (CUDA kernels behind the C ABI in
 include/gdn.h); this package is its thin Python binding plus the seeded
