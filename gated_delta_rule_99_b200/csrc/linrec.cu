@@ -227,17 +227,17 @@ __device__ __forceinline__ void copy_rows(E *dst, const E *src, int64_t stride, 
             }
     } else {
 #pragma unroll 1
-        for (int i = 0; i < kSpan; i += 4) {
-            E v[4][2];
+        for (int i = 0; i < kSpan; i += 8) {
+            E v[8][2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 8; ++r)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int c = lane + 32 * j;
                     v[r][j] = i + r < rows && c < cols ? src[(i + r) * stride + c] : E(0.f);
                 }
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 8; ++r)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) dst[(i + r) * kCh + lane + 32 * j] = v[r][j];
         }
