@@ -167,9 +167,16 @@ def _desc_from(q, v, cu_host, scale, flags=0):
     return make_desc(B, T, H, K, V, n_seqs, dt, scale, flags), (B, T, H, K, V, n_seqs)
 
 
+def _check_mirror(cu_seqlens_host):
+    """The library reads the mirror on the host: an address on a device would end the process."""
+    if cu_seqlens_host is not None and cu_seqlens_host.device.type != "cpu":
+        raise ValueError("cu_seqlens_host must be a CPU tensor, got one on %s" % cu_seqlens_host.device)
+
+
 def _seqlens(cu_seqlens, cu_seqlens_host, device):
     if cu_seqlens is None and cu_seqlens_host is None:
         return None, None
+    _check_mirror(cu_seqlens_host)
     host = cu_seqlens_host if cu_seqlens_host is not None else cu_seqlens.cpu()
     host = host.to(torch.int32).contiguous()
     dev = cu_seqlens if cu_seqlens is not None and cu_seqlens.is_cuda else host.to(device)
@@ -424,6 +431,8 @@ def _offsets(cu_seqlens, cu_seqlens_host, index):
                              % (cu_seqlens.device, index))
         cu_seqlens, cu_seqlens_host = _seqlens(cu_seqlens, cu_seqlens_host,
                                                torch.device("cuda", index))
+    else:
+        _check_mirror(cu_seqlens_host)
     if cu_seqlens.shape != cu_seqlens_host.shape or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must have one dimension and 2 values or more, and its host "
                          "mirror the same number")

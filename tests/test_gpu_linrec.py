@@ -419,3 +419,18 @@ def test_empty_rows_pass_the_states_through():
     assert o.shape == x.shape and torch.equal(hT, h0)
     dh0 = gdn.gdn_linrec_bwd(x, x, x, cu_seqlens=cu.cuda(), cu_seqlens_host=cu, dhT=dhT)[2]
     assert torch.equal(dh0, dhT)
+
+
+def test_a_device_tensor_as_the_mirror_of_the_offsets_is_refused():
+    v = draw(1, 30, 8, N=2)
+    d = {k: t.cuda() for k, t in v.items()}
+    cu = torch.tensor([0, 10, 30], dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 30, 1, 64, device="cuda")
+    s = torch.zeros(1, 30, 1, device="cuda")
+    for call in (lambda **k: gdn.gdn_linrec_fwd(d["x"], d["g"], **k),
+                 lambda **k: gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], **k),
+                 lambda **k: gdn.gdn_fwd(q, q, q, s, s, **k),
+                 lambda **k: gdn.gdn_bwd(q, q, q, s, s, q, **k)):
+        for kw in (dict(cu_seqlens=cu), dict()):
+            with pytest.raises(ValueError, match="CPU tensor"):
+                call(cu_seqlens_host=cu, **kw)

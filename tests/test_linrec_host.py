@@ -174,3 +174,16 @@ def test_token_strides():
         stride(wide, (2, 5, 25))
     with pytest.raises(ValueError):
         _row_stride(wide, "x", torch.bfloat16, (2, 5, 24))
+
+
+def test_the_mirror_of_the_offsets_must_be_on_the_host():
+    from gated_delta_rule_99_b200._binding import _offsets, _seqlens
+
+    cu = torch.tensor([0, 3, 8], dtype=torch.int32)
+    elsewhere = torch.empty(3, dtype=torch.int32, device="meta")  # no host address either
+    for call in (lambda: _offsets(cu, elsewhere, -1), lambda: _offsets(None, elsewhere, 0),
+                 lambda: _offsets(cu.long(), elsewhere, 0), lambda: _seqlens(cu, elsewhere, "cpu"),
+                 lambda: _seqlens(None, elsewhere.long(), "cpu")):
+        with pytest.raises(ValueError, match="cu_seqlens_host must be a CPU tensor"):
+            call()
+    assert _offsets(cu, cu.clone(), -1)[3] == 2
