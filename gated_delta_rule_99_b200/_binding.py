@@ -509,10 +509,14 @@ def gdn_linrec_bwd(x, g, do, cu_seqlens=None, h0=None, dhT=None, complement=Fals
     return dx, dg, dh0
 
 
-def linrec_status(stream=None) -> int:
-    """Status code of this device's gdn_linrec_fwd and gdn_linrec_bwd calls (0: ok), after
-    waiting for the stream; reading clears it."""
-    return int(lib().gdn_linrec_status(_stream(stream)))
+def linrec_status(stream=None, device=None) -> int:
+    """Status code of a device's gdn_linrec_fwd and gdn_linrec_bwd calls (0: ok), after waiting
+    for the stream; reading clears it.  The device is the stream's; without a stream the current
+    stream of ``device`` is taken (a device, its index or a tensor on it; None: the current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device.device if isinstance(device, torch.Tensor) else device)
+    with torch.cuda.device(stream.device):
+        return int(lib().gdn_linrec_status(ctypes.c_void_p(stream.cuda_stream)))
 
 
 def gdn_linrec_decode(x, g, state, complement=False, o=None, stream=None):

@@ -187,3 +187,44 @@ def test_the_mirror_of_the_offsets_must_be_on_the_host():
         with pytest.raises(ValueError, match="cu_seqlens_host must be a CPU tensor"):
             call()
     assert _offsets(cu, cu.clone(), -1)[3] == 2
+
+
+def test_the_status_is_read_on_the_device_of_the_calls(monkeypatch):
+    """The calls run on their tensors' device, whatever the current one is; so does the read of
+    their status.  Two devices, with a timeout on the second one."""
+    from gated_delta_rule_99_b200 import _binding
+
+    class Stream:
+        def __init__(self, index, handle):
+            self.device, self.cuda_stream = torch.device("cuda", index), handle
+
+    class Device:
+        current = 0
+
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, Device.current = Device.current, self.index
+
+        def __exit__(self, *exc):
+            Device.current = self.before
+
+    class Lib:
+        calls = []
+
+        def gdn_linrec_status(self, stream):
+            self.calls.append((Device.current, stream.value))
+            return 6 if Device.current == 1 else 0
+
+    def current_stream(device=None):
+        index = Device.current if device is None else device if isinstance(device, int) else device.index
+        return Stream(index, 100 + index)
+
+    monkeypatch.setattr(_binding, "lib", Lib)
+    monkeypatch.setattr(torch.cuda, "current_stream", current_stream)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    assert gdn.linrec_status() == 0
+    assert gdn.linrec_status(Stream(1, 7)) == 6 and gdn.linrec_status(stream=Stream(0, 9)) == 0
+    assert gdn.linrec_status(device=1) == 6 and gdn.linrec_status(device=torch.device("cuda", 1)) == 6
+    assert Lib.calls == [(0, 100), (1, 7), (0, 9), (1, 101), (1, 101)] and Device.current == 0
