@@ -409,7 +409,8 @@ struct Shared {
     uint64_t bar[2];                        // arrivals of the cluster's maps (even, odd steps)
     int cut[kWarps];                        // bit 0: a start in the span, bit 1: an end
     int start_of[kWarps][kMaxSpan], end_of[kWarps][kMaxSpan];
-    int dead;                               // a wait ran out
+    int dead;                               // the step in which a wait ran out, counted from 1 (0: none)
+    int sent[kMaxCluster];                  // steps whose maps each CTA sends: all, or what one that gave up says
     int32_t cu[kCuKept];                    // the offsets of few documents: crossing one costs no global loads
 };
 constexpr size_t kSmemCta = sizeof(Shared) + 1024;  // of a CTA beside tiles and maps (1 KB is the system's)
@@ -430,18 +431,24 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, uint32_t
     }
     return false;
 }
-__device__ __forceinline__ void give_up(Shared &sh) {
-    sh.dead = 1;
+__device__ __forceinline__ void give_up(Shared &sh, int step) {
+    sh.dead = step + 1;
     g_status = kDevTimeout;
 }
 
+// Whether the planted failure makes this CTA wait for 16 bytes that no one sends.
+__device__ __forceinline__ bool stalls(const LinrecParams &p, int step) {
+    return p.test_hook == GDN_TEST_STALL_COPY && blockIdx.x == 0 && step == 0;
+}
+
 // Makes the mbarriers ready in every CTA of the cluster before anyone sends.
-__device__ __forceinline__ void cluster_begin(const LinrecParams &p, Shared &sh, int cluster) {
+__device__ __forceinline__ void cluster_begin(const LinrecParams &p, Shared &sh, int cluster, int steps) {
     if (p.cu && p.N < kCuKept)
         for (int i = threadIdx.x; i <= p.N; i += kThreads) sh.cu[i] = p.cu[i];
     if (threadIdx.x == 0) {
         sh.dead = 0;
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.bar[i], 1);
+        for (int i = 0; i < kMaxCluster; ++i) sh.sent[i] = steps;
         ptx::fence_mbar_init();
     }
     __syncthreads();
@@ -450,15 +457,35 @@ __device__ __forceinline__ void cluster_begin(const LinrecParams &p, Shared &sh,
 __device__ __forceinline__ void cluster_ready(int cluster) {
     if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// No CTA leaves while another may still send to it.  One that gave up has not seen all maps arrive: half a
-// millisecond for those on their way, to it or from it.
-__device__ __forceinline__ void cluster_end(const Shared &sh, int cluster) {
-    if (cluster > 1) {
-        if (sh.dead)
-            for (int i = 0; i < 512; ++i) __nanosleep(1000);
+// No CTA leaves while a map may still arrive in it.  One that has made all its steps has seen all maps.  One that
+// gave up in a step has sent its maps up to that step's, which it tells the others before the barrier; behind the
+// barrier it knows how many maps come, makes up for those that do not, and waits (up to `limit` polls) for the rest.
+__device__ __forceinline__ void count_maps(Shared &sh, int cluster, int step, uint32_t extra, uint32_t limit) {
+    uint32_t now = 0, next = 0;  // maps of this step and, of CTAs that went on, of the one after it
+    for (int r = 0; r < cluster; ++r) now += sh.sent[r] > step, next += sh.sent[r] > step + 1;
+    const uint32_t missing = (cluster - now) * (uint32_t)sizeof(Map) + extra;
+    uint64_t *bar = &sh.bar[step & 1], *other = &sh.bar[(step + 1) & 1];
+    if (missing)
+        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(missing) : "memory");
+    if (next) ptx::mbar_arrive_expect_tx(other, next * (uint32_t)sizeof(Map));
+    arrived(bar, (step >> 1) & 1, limit);
+    if (next) arrived(other, (step + 1) >> 1 & 1, limit);
+}
+__device__ __forceinline__ void cluster_end(const LinrecParams &p, Shared &sh, int cluster) {
+    if (cluster == 1) return;
+    const int sent = sh.dead;
+    if (!sent) {
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        return;
     }
+    const int i = threadIdx.x;
+    if (i < cluster)
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(&sh.sent[blockIdx.x % p.cluster], i)), "r"(sent) : "memory");
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (i == 0) count_maps(sh, cluster, sent - 1, stalls(p, sent - 1) ? 16 : 0, kWaitLimit);
 }
 
 // The carrying warp's part of a step, between the CTA's two barriers: sends the tile's map q to
@@ -468,8 +495,7 @@ __device__ __forceinline__ void send_map(const LinrecParams &p, Shared &sh, Map 
     if (p.cluster == 1) return;
     const int buf = step & 1;
     if (lane == 0) {
-        const bool stall = p.test_hook == GDN_TEST_STALL_COPY && blockIdx.x == 0 && step == 0;
-        ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * (uint32_t)sizeof(Map) + (stall ? 16 : 0));
+        ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * (uint32_t)sizeof(Map) + (stalls(p, step) ? 16 : 0));
     }
     if (cut) q.x = -0.f;
     const Map *to = maps + buf * p.cluster + rank;
@@ -487,7 +513,7 @@ __device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, cons
     }
     const int buf = step & 1;
     if (!__all_sync(0xffffffffu, arrived(&sh.bar[buf], (step >> 1) & 1, p.wait_limit))) {
-        if (lane == 0) give_up(sh);
+        if (lane == 0) give_up(sh, step);
         return;
     }
     const Map *from = maps + buf * p.cluster;
@@ -587,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __gr
     unsigned char *mine = smem + warp * stages * kBytes;
     Map *maps = reinterpret_cast<Map *>(smem + kWarps * stages * kBytes);
     const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
-    cluster_begin(p, sh, cluster);
+    cluster_begin(p, sh, cluster, u.steps);
 
     uint32_t t0 = u.rank * kTile + warp * kSpan, ahead = t0;  // the warp's first token of a step, and of the next copies
     Copies<kSpan, T> cx;
@@ -691,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_fwd_kernel(const __gr
     }
     copy_wait(0);
     pass_empty(p, u, p.h0, p.hT, warp, lane);
-    cluster_end(sh, cluster);
+    cluster_end(p, sh, cluster);
 }
 
 // ---------------------------------------------------------------- backward
@@ -758,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __gr
     unsigned char *mine = smem + warp * stages * kBytes;
     Map *maps = reinterpret_cast<Map *>(smem + kWarps * stages * kBytes);
     const int *start_of = sh.start_of[warp], *end_of = sh.end_of[warp];
-    cluster_begin(p, sh, cluster);
+    cluster_begin(p, sh, cluster, u.steps);
 
     // steps go from the stream's end
     uint32_t t0 = ((uint32_t)(u.steps - 1) * cluster + u.rank) * kTile + warp * kSpan, ahead = t0;
@@ -900,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) linrec_bwd_kernel(const __gr
     }
     copy_wait(0);
     pass_empty(p, u, p.dhT, p.dh0, warp, lane);
-    cluster_end(sh, cluster);
+    cluster_end(p, sh, cluster);
 }
 
 // ---------------------------------------------------------------- one-token form

@@ -434,3 +434,33 @@ def test_a_device_tensor_as_the_mirror_of_the_offsets_is_refused():
         for kw in (dict(cu_seqlens=cu), dict()):
             with pytest.raises(ValueError, match="CPU tensor"):
                 call(cu_seqlens_host=cu, **kw)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("B,T,D", [(1, 200, 64), (1, 1100, 8), (1, 9000, 64), (3, 5000, 130), (2, 40000, 66)])
+def test_clusters_that_give_up_end_with_every_map_accounted_for(B, T, D, types):
+    """Waits that run out in the first step (planted), or wherever a limit of few polls makes them: clusters
+    of one step and of many, in both directions.  The calls end, and the ones after them are right."""
+    v = draw(B, T, D, *types, seed=T)
+    d = {k: t.cuda() for k, t in v.items()}
+    run = lambda: gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], states=gdn.gdn_linrec_fwd(
+        d["x"], d["g"], h0=d["h0"], save_states=True)[2], h0=d["h0"], dhT=d["dhT"])
+    want = run()
+    gdn.linrec_status()
+    try:
+        gdn.set_wait_limit(256)
+        gdn.set_test_hook(gdn.GDN_TEST_STALL_COPY)
+        run()
+        assert gdn.linrec_status() == 6
+        gdn.set_test_hook(0)
+        for polls in (1, 2, 5, 20):
+            gdn.set_wait_limit(polls)
+            for _ in range(5):
+                run()
+            assert gdn.linrec_status() in (0, 6)
+    finally:
+        gdn.set_test_hook(0)
+        gdn.set_wait_limit(0)
+    for a, b in zip(run(), want):
+        assert torch.equal(a, b)
+    assert gdn.linrec_status() == 0
