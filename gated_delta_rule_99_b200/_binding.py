@@ -510,9 +510,10 @@ def gdn_linrec_bwd(x, g, do, cu_seqlens=None, h0=None, dhT=None, complement=Fals
 
 
 def linrec_status(stream=None, device=None) -> int:
-    """Status code of a device's gdn_linrec_fwd and gdn_linrec_bwd calls (0: ok), after waiting
-    for the stream; reading clears it.  The device is the stream's; without a stream the current
-    stream of ``device`` is taken (a device, its index or a tensor on it; None: the current one)."""
+    """Status code (0: ok) of the gdn_linrec_fwd and gdn_linrec_bwd calls on the stream, and of
+    captured ones replayed on its device, after waiting for the stream.  Each timeout is told once to
+    every host thread that asks.  Without a stream the current stream of ``device`` is taken (a
+    device, its index or a tensor on it; None: the current one)."""
     if stream is None:
         stream = torch.cuda.current_stream(device.device if isinstance(device, torch.Tensor) else device)
     with torch.cuda.device(stream.device):

@@ -65,6 +65,7 @@ struct LinrecParams {
     int64_t x_step, g_step, dy_step, o_step, dx_step, dg_step;
     uint32_t wait_limit;
     int32_t test_hook;
+    int32_t slot;    // of g_gave_up
     int32_t single;  // every stream is one sequence
     const int32_t *cu;
     const void *x, *g, *dy;
@@ -255,8 +256,11 @@ __device__ __forceinline__ void send(uint32_t to, float4 v, uint32_t bar) {
                  ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar) : "memory");
 }
 
-// Status of this device's calls (gdn_linrec_status).
-__device__ int32_t g_status;
+// Waits of this device's calls that gave up (gdn_linrec_status), counted by the stream of the call, so that no
+// stream's calls are taken for another's (two of 4095 may fall together); slot 0: captured calls, which replay
+// on any stream.  Counts are never cleared: what one reader is told is not lost to the others.
+constexpr int kSlots = 4096;
+__device__ uint32_t g_gave_up[kSlots];
 
 // ---------------------------------------------------------------- sequences of a stream
 // The sequence that holds a token, for a whole warp: index n, tokens [beg, end) of the stream.
@@ -431,9 +435,9 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity, uint32_t
     }
     return false;
 }
-__device__ __forceinline__ void give_up(Shared &sh, int step) {
+__device__ __forceinline__ void give_up(const LinrecParams &p, Shared &sh, int step) {
     sh.dead = step + 1;
-    g_status = kDevTimeout;
+    atomicAdd(&g_gave_up[p.slot], 1u);
 }
 
 // Whether the planted failure makes this CTA wait for 16 bytes that no one sends.
@@ -513,7 +517,7 @@ __device__ __forceinline__ void carry_on(const LinrecParams &p, Shared &sh, cons
     }
     const int buf = step & 1;
     if (!__all_sync(0xffffffffu, arrived(&sh.bar[buf], (step >> 1) & 1, p.wait_limit))) {
-        if (lane == 0) give_up(sh, step);
+        if (lane == 0) give_up(p, sh, step);
         return;
     }
     const Map *from = maps + buf * p.cluster;
@@ -1033,6 +1037,36 @@ cudaError_t fit_of(Kernel kernel, Fit *fits, const Fit **out) {
     return e;
 }
 
+bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) cudaGetLastError();  // the launch will say
+    return cap != cudaStreamCaptureStatusNone;
+}
+int stream_slot(cudaStream_t s) {
+    return 1 + (int)((reinterpret_cast<uintptr_t>(s) * 0x9E3779B97F4A7C15ull >> 32) % (kSlots - 1));
+}
+int slot_of(cudaStream_t s) { return capturing(s) ? 0 : stream_slot(s); }
+
+// Whether this host thread has not been told of this count yet.  It remembers the last 64 slots it asked for.
+bool is_news(int device, int slot, uint32_t count) {
+    struct Told {
+        int device, slot;
+        uint32_t count;
+    };
+    constexpr int kTold = 64;
+    thread_local Told told[kTold];  // slot 0 of device 0 with count 0 where unused
+    thread_local int next = 0;
+    for (Told &t : told)
+        if (t.device == device && t.slot == slot) {
+            const bool news = t.count != count;
+            t.count = count;
+            return news;
+        }
+    told[next] = {device, slot, count};
+    next = (next + 1) % kTold;
+    return count != 0;
+}
+
 // A kernel of `smem` bytes of dynamic shared memory on p's clusters.
 cudaError_t launch_cluster(Kernel kernel, const LinrecParams &p, size_t smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -1078,6 +1112,7 @@ cudaError_t launch_typed(LinrecParams p, Pass pass, cudaStream_t s) {
     p.dx_step = tokens * p.dx_row, p.dg_step = tokens * p.dg_row;
     p.wait_limit = call_wait_limit();
     p.test_hook = call_test_hook();
+    p.slot = slot_of(s);
     GDN_LAUNCH(fwd ? kKLinrecFwd : kKLinrecBwd, s, (err = launch_cluster(kernel, p, smem, s)));
     return err;
 }
@@ -1201,12 +1236,20 @@ extern "C" {
 
 gdn_status gdn_linrec_status(void *stream) {
     using namespace gdn;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GDN_ERR_CUDA;
-    int32_t status = 0;
-    if (cudaMemcpyFromSymbol(&status, g_status, sizeof(status)) != cudaSuccess) return GDN_ERR_CUDA;
-    const int32_t zero = 0;
-    if (status != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return GDN_ERR_CUDA;
-    return static_cast<gdn_status>(status);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (capturing(s)) return GDN_ERR_INVALID_ARG;
+    int device = 0;
+    void *at = nullptr;
+    if (cudaGetDevice(&device) != cudaSuccess || cudaGetSymbolAddress(&at, g_gave_up) != cudaSuccess) return GDN_ERR_CUDA;
+    const uint32_t *counts = static_cast<const uint32_t *>(at);
+    const int slot = stream_slot(s);
+    uint32_t own = 0, captured = 0;
+    if (cudaMemcpyAsync(&own, counts + slot, sizeof(own), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemcpyAsync(&captured, counts, sizeof(captured), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    const bool one = is_news(device, slot, own), two = is_news(device, 0, captured);
+    return one || two ? GDN_ERR_TIMEOUT : GDN_OK;
 }
 
 size_t gdn_linrec_states_size(const gdn_linrec_desc *desc) {

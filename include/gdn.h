@@ -270,10 +270,13 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void
                           float *dh0, const float *states, void *workspace,
                           size_t workspace_bytes, void *stream);
 
-/* Synchronises the stream, then returns and clears the device-side status of
- * the gdn_linrec_fwd and gdn_linrec_bwd calls on the current device: GDN_OK, or
- * GDN_ERR_TIMEOUT when a bounded wait between the CTAs of a cluster ran out (the
- * call's outputs are then undefined).  GDN_ERR_CUDA if the stream failed. */
+/* Synchronises the stream, then returns GDN_ERR_TIMEOUT if a bounded wait between
+ * the CTAs of a cluster ran out in one of the gdn_linrec_fwd and gdn_linrec_bwd calls
+ * on that stream, or in a replay of captured ones on any stream of the current
+ * device, that the calling host thread has not been told of (the outputs of such
+ * a call are undefined); else GDN_OK.  Reading takes nothing from other threads or
+ * streams.  The stream belongs to the current device and is not being captured
+ * (GDN_ERR_INVALID_ARG).  GDN_ERR_CUDA if the stream failed. */
 gdn_status gdn_linrec_status(void *stream);
 
 /* One-token form for inference: advances state [B][D] (fp32, in place) through

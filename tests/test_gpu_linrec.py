@@ -464,3 +464,52 @@ def test_clusters_that_give_up_end_with_every_map_accounted_for(B, T, D, types):
     for a, b in zip(run(), want):
         assert torch.equal(a, b)
     assert gdn.linrec_status() == 0
+
+
+def test_a_timeout_is_told_of_its_own_stream_and_to_every_thread():
+    from concurrent.futures import ThreadPoolExecutor
+    v = draw(1, 2000, 64, seed=4)
+    x, g = v["x"].cuda(), v["g"].cuda()
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+
+    def stalled(call):
+        gdn.set_wait_limit(256)
+        gdn.set_test_hook(gdn.GDN_TEST_STALL_COPY)
+        try:
+            call()
+        finally:
+            gdn.set_test_hook(0)
+            gdn.set_wait_limit(0)
+
+    with ThreadPoolExecutor(1) as other:
+        there = lambda *args: other.submit(gdn.linrec_status, *args).result()
+        for s in (a, b, c):
+            assert gdn.linrec_status(s) == 0 and there(s) == 0
+        stalled(lambda: gdn.gdn_linrec_fwd(x, g, stream=a))
+        gdn.gdn_linrec_fwd(x, g, stream=b)
+        assert gdn.linrec_status(b) == 0
+        assert gdn.linrec_status(a) == 6 and gdn.linrec_status(a) == 0
+        assert there(b) == 0 and there(a) == 6 and there(a) == 0
+        # captured calls: told of whichever stream is asked for, once to each thread
+        graph = torch.cuda.CUDAGraph()
+
+        def capture():
+            with torch.cuda.graph(graph):
+                gdn.gdn_linrec_fwd(x, g)
+
+        stalled(capture)
+        with torch.cuda.stream(c):
+            graph.replay()
+        assert gdn.linrec_status(c) == 6 and gdn.linrec_status(c) == 0 and gdn.linrec_status(b) == 0
+        assert there(c) == 6 and there(c) == 0
+
+
+def test_the_status_of_a_stream_that_is_captured_is_refused():
+    x = torch.zeros(1, 300, 64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, _ = gdn.gdn_linrec_fwd(x, x)
+        assert gdn.linrec_status() == 1
+    graph.replay()
+    assert gdn.linrec_status() == 0 and (o == 0).all()
