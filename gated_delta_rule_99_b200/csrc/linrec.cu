@@ -501,7 +501,7 @@ __device__ __forceinline__ void send_map(const LinrecParams &p, Shared &sh, Map 
     if (lane == 0) {
         ptx::mbar_arrive_expect_tx(&sh.bar[buf], p.cluster * (uint32_t)sizeof(Map) + (stalls(p, step) ? 16 : 0));
     }
-    if (cut) q.x = -0.f;
+    q.x = __uint_as_float((__float_as_uint(q.x) & 0x7fffffffu) | (cut ? 0x80000000u : 0u));
     const Map *to = maps + buf * p.cluster + rank;
     for (int i = 1; i <= p.cluster; ++i) {  // to the neighbour first, so that no CTA is everyone's first
         const int r = rank + i < p.cluster ? rank + i : rank + i - p.cluster;

@@ -513,3 +513,44 @@ def test_the_status_of_a_stream_that_is_captured_is_refused():
         assert gdn.linrec_status() == 1
     graph.replay()
     assert gdn.linrec_status() == 0 and (o == 0).all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("lengths", [None, [700, 0, 4100, 1, 4199]])
+def test_gates_that_are_nan_stay_in_their_channel(types, complement, lengths):
+    """NaN of both signs in g, in tiles of several CTAs of a cluster: the channel beside it (in the same lane)
+    and the other documents keep their bits."""
+    T, D = 9000, 66
+    N = 1 if lengths is None else len(lengths)
+    v = draw(1, T, D, *types, N=N, seed=3)
+    d = {k: t.cuda() for k, t in v.items()}
+    cu = None if lengths is None else torch.tensor([0] + np.cumsum(lengths).tolist(), dtype=torch.int32)
+    kw = dict(cu_seqlens=None if cu is None else cu.cuda(), cu_seqlens_host=cu, h0=d["h0"], complement=complement)
+
+    def run():
+        o, hT, states = gdn.gdn_linrec_fwd(d["x"], d["g"], save_states=True, **kw)
+        return (o, hT) + gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], dhT=d["dhT"], states=states, **kw)
+
+    want = run()
+    nan = torch.tensor([float("nan")])
+    at = {0: 5, 3: 1000, 33: 4500, 64: 8500, 65: 8500}
+    for i, (c, t) in enumerate(at.items()):
+        d["g"][0, t, c] = torch.copysign(nan, torch.tensor(1.0 - 2 * (i % 2))).to(d["g"].dtype).item()
+    assert d["g"].isnan().sum() == len(at)
+    o, hT, dx, dg, dh0 = run()
+    segs = ref.segments(1, T, None if cu is None else cu.tolist())
+    for c in range(D):
+        t = at.get(c)
+        n, (t0, t1) = (-1, (0, 0)) if t is None else next((n, s) for n, s in enumerate(segs) if s[0] <= t < s[1])
+        here = torch.zeros(T, dtype=torch.bool, device="cuda")
+        here[t0:t1] = True  # the document of the NaN, and in it the tokens from it on, or up to it
+        late, early = here.clone(), here.clone()
+        if t is not None:
+            late[:t] = False
+            early[t + complement:] = False  # dx of the token itself has the factor 1 - exp(NaN)
+        for got, ref_, bad in ((o, want[0], late), (dx, want[2], early), (dg, want[3], here)):
+            assert got[0, bad, c].isnan().all() and torch.equal(got[0, ~bad, c], ref_[0, ~bad, c])
+        for got, ref_ in ((hT, want[1]), (dh0, want[4])):
+            for m in range(N):
+                assert got[m, c].isnan() if m == n else got[m, c] == ref_[m, c]
