@@ -3,8 +3,9 @@
 #include <cudaTypedefs.h>
 
 #include <cstring>
+#include <memory>
 #include <mutex>
-#include <vector>
+#include <new>
 
 #include "gdn_internal.cuh"
 
@@ -85,14 +86,16 @@ gdn_status check_seqlens(const gdn_desc *d, const int32_t *cu_dev, const int32_t
     }
     if (!cu_dev) return GDN_ERR_INVALID_ARG;
     if (misaligned(cu_dev, 4)) return GDN_ERR_ALIGNMENT;
-    std::vector<int32_t> copy;
+    std::unique_ptr<int32_t[]> copy;
     if (!cu_host) {
-        copy.resize((size_t)d->n_seqs + 1);
-        if (cudaMemcpyAsync(copy.data(), cu_dev, sizeof(int32_t) * copy.size(),
+        const size_t n = (size_t)d->n_seqs + 1;
+        copy.reset(new (std::nothrow) int32_t[n]);  // no exception leaves a C entry
+        if (!copy) return GDN_ERR_CUDA;
+        if (cudaMemcpyAsync(copy.get(), cu_dev, sizeof(int32_t) * n,
                             cudaMemcpyDeviceToHost, stream) != cudaSuccess)
             return GDN_ERR_CUDA;
         if (cudaStreamSynchronize(stream) != cudaSuccess) return GDN_ERR_CUDA;
-        cu_host = copy.data();
+        cu_host = copy.get();
     }
     if (cu_host[0] != 0 || cu_host[d->n_seqs] != d->T) return GDN_ERR_INVALID_ARG;
     int64_t nc = 0;

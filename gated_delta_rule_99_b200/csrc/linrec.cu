@@ -30,8 +30,9 @@
 // enter each token: the forward leaves the state entering every 64th token (4 / 64 bytes per
 // element), from which a tile recomputes its own.
 #include <atomic>
+#include <memory>
 #include <mutex>
-#include <vector>
+#include <new>
 
 #include "gdn_internal.cuh"
 #include "tc_ptx.cuh"
@@ -1211,17 +1212,19 @@ gdn_status check_seqlens(const gdn_linrec_desc *d, const int32_t *cu_dev, const 
     if (d->n_seqs == 0) return cu_dev || cu_host ? GDN_ERR_INVALID_ARG : GDN_OK;
     if (!cu_dev) return GDN_ERR_INVALID_ARG;
     if (mis(cu_dev, 4)) return GDN_ERR_ALIGNMENT;
-    std::vector<int32_t> copy;
+    std::unique_ptr<int32_t[]> copy;
     if (!cu_host) {
         cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
         if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return GDN_ERR_CUDA;
         if (cap != cudaStreamCaptureStatusNone) return GDN_ERR_INVALID_ARG;
-        copy.resize((size_t)d->n_seqs + 1);
-        if (cudaMemcpyAsync(copy.data(), cu_dev, sizeof(int32_t) * copy.size(),
+        const size_t n = (size_t)d->n_seqs + 1;
+        copy.reset(new (std::nothrow) int32_t[n]);  // no exception leaves a C entry
+        if (!copy) return GDN_ERR_CUDA;
+        if (cudaMemcpyAsync(copy.get(), cu_dev, sizeof(int32_t) * n,
                             cudaMemcpyDeviceToHost, s) != cudaSuccess ||
             cudaStreamSynchronize(s) != cudaSuccess)
             return GDN_ERR_CUDA;
-        cu_host = copy.data();
+        cu_host = copy.get();
     }
     if (cu_host[0] != 0 || cu_host[d->n_seqs] != d->T) return GDN_ERR_INVALID_ARG;
     for (int64_t n = 0; n < d->n_seqs; ++n)

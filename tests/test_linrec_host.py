@@ -228,3 +228,25 @@ def test_the_status_is_read_on_the_device_of_the_calls(monkeypatch):
     assert gdn.linrec_status(Stream(1, 7)) == 6 and gdn.linrec_status(stream=Stream(0, 9)) == 0
     assert gdn.linrec_status(device=1) == 6 and gdn.linrec_status(device=torch.device("cuda", 1)) == 6
     assert Lib.calls == [(0, 100), (1, 7), (0, 9), (1, 101), (1, 101)] and Device.current == 0
+
+
+def test_offsets_too_many_for_the_host_are_an_error_code():
+    """Without the mirror the offsets are copied to the host: where their memory cannot be had, the call
+    returns an error, and the process goes on.  In a process of its own, whose address space is limited."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import ctypes, resource
+import gated_delta_rule_99_b200 as gdn
+L, fake, n = gdn.lib(), 0x7F0000000000, 1 << 29
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (1 << 30), used + (1 << 30)))
+d = gdn.make_desc(1, 100, 1, 64, 64, n_seqs=n)
+print(L.gdn_fwd(ctypes.byref(d), fake, fake, fake, fake, fake, fake, None, None, fake, None, fake, 1 << 60, None))
+d = gdn.GdnLinrecDesc(1, 100, 64, (1 << 31) - 1, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+print(L.gdn_linrec_fwd(ctypes.byref(d), fake, fake, fake, None, None, fake, None, None, None))
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.split() == ["5", "5"], r.stdout + r.stderr[-2000:]
