@@ -180,6 +180,8 @@ def _seqlens(cu_seqlens, cu_seqlens_host, device):
     host = cu_seqlens_host if cu_seqlens_host is not None else cu_seqlens.cpu()
     host = host.to(torch.int32).contiguous()
     dev = cu_seqlens if cu_seqlens is not None and cu_seqlens.is_cuda else host.to(device)
+    if dev.numel() < host.numel():  # the kernels read as many offsets as the mirror has
+        raise ValueError("cu_seqlens has %d values, its host mirror %d" % (dev.numel(), host.numel()))
     return dev.to(torch.int32).contiguous(), host
 
 

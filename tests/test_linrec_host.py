@@ -250,3 +250,15 @@ print(L.gdn_linrec_fwd(ctypes.byref(d), fake, fake, fake, None, None, fake, None
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.split() == ["5", "5"], r.stdout + r.stderr[-2000:]
+
+
+def test_device_offsets_must_be_as_many_as_the_mirrors():
+    from gated_delta_rule_99_b200._binding import _seqlens
+
+    class OnDevice(torch.Tensor):
+        is_cuda = True
+
+    cu = torch.tensor([0, 3, 8, 9], dtype=torch.int32)
+    with pytest.raises(ValueError, match="3 values, its host mirror 4"):
+        _seqlens(cu[:3].as_subclass(OnDevice), cu, "cpu")
+    assert _seqlens(cu.as_subclass(OnDevice), cu[:3], "cpu")[1].numel() == 3
