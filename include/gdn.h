@@ -300,7 +300,10 @@ gdn_status gdn_linrec_decode(const gdn_linrec_desc *desc, const void *x, const v
  * are not turned.  p is the token's position (int32, any sign), or its index in
  * its row with positions NULL; the angle is formed and reduced in 64 bits, so
  * far positions are exact.  Norms and rotations are in fp32, rounded once to dtype.
- * |x|^2 is an fp32 sum: a row whose sum underflows to 0 counts as a zero row.
+ * |x|^2 is an fp32 sum, as GDN_FLAG_QK_L2NORM's.  A row whose sum underflows to 0
+ * counts as a zero row, and below about 2^-100 the sum loses bits (where eps does
+ * not cover it).  A row whose sum passes the fp32 maximum (with a value above
+ * 2^64 = 1.8e19, say) has r = 0: its results are 0, its gradients 0 or NaN.
  *
  * Layouts: q, qo, dqo, dq [B][T][Hq][d] and k, ko, dko, dk [B][T][Hk][d] in
  * dtype, a token's heads adjacent; the strides give the elements from one token

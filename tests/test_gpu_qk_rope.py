@@ -321,3 +321,24 @@ def test_planted_launch_failure_is_reported():
     finally:
         gdn.set_test_hook(0)
     run_and_check(v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+def test_rows_whose_sum_of_squares_passes_fp32(norm, dtype):
+    """Rows of 1e18 are right (64 squares sum to 6e37); rows of 1e20, whose sum is infinite, have r = 0:
+    zeros, and zero gradients, and their neighbours are as ever."""
+    v = draw(1, 12, 2, 2, 64, 64, dtype, weights=norm == "rms")
+    v["q"][0, 6] *= 1e18 / 4
+    want = run_and_check(v, norm)
+    far = {n: None if t is None else t.clone() for n, t in v.items()}
+    far["q"][0, 3, 1] = 1e20
+    far["k"][0, 5, 0] = -1e20
+    dev = {n: None if t is None else t.cuda() for n, t in far.items()}
+    kw = dict(norm=norm, **{n: dev[n] for n in ("inv_freq", "q_weight", "k_weight")})
+    got = gdn.gdn_qk_norm_rope_fwd(dev["q"], dev["k"], **kw)
+    got += gdn.gdn_qk_norm_rope_bwd(dev["q"], dev["k"], dev["dqo"], dev["dko"], **kw)[:2]
+    for a, b, row in zip(got, want, ((0, 3, 1), (0, 5, 0)) * 2):
+        assert (a[row] == 0).all()
+        a[row] = b[row]
+        assert torch.equal(a, b)
