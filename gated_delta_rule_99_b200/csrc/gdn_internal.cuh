@@ -188,6 +188,8 @@ enum KernelId : int32_t {
     kKQkRope,
     kKQkRopeBwd,
     kKQkRopeDw,
+    kKQkRopeGroup,
+    kKQkRopeBwdGroup,
     kKernelCount
 };
 

@@ -608,10 +608,10 @@ cudaError_t launch_units(QkParams p, bool bwd, cudaStream_t s) {
                                         : full ? qk_kernel<T, V, NU, VEC, ADJ, true, kVariants, kVariants>
                                                : qk_kernel<T, V, NU, VEC, ADJ, true, kVariants, false>;
     if (!bwd) {
-        if (p.tokens) GDN_LAUNCH(kKQkRope, s, kernel<<<grid, kThreads, 0, s>>>(p));
+        if (p.tokens) GDN_LAUNCH(group ? kKQkRopeGroup : kKQkRope, s, kernel<<<grid, kThreads, 0, s>>>(p));
         return cudaSuccess;
     }
-    if (p.tokens || p.dw[0] || p.dw[1]) GDN_LAUNCH(kKQkRopeBwd, s, kernel<<<grid, kThreads, 0, s>>>(p));
+    if (p.tokens || p.dw[0] || p.dw[1]) GDN_LAUNCH(group ? kKQkRopeBwdGroup : kKQkRopeBwd, s, kernel<<<grid, kThreads, 0, s>>>(p));
     if (p.dw[0] || p.dw[1])
         GDN_LAUNCH(kKQkRopeDw, s, qk_dw_kernel<<<dim3((p.d + 31) / 32, 2), dim3(32, 32), 0, s>>>(p));
     return cudaSuccess;

@@ -14,7 +14,7 @@ const char *const kNames[kKernelCount] = {
     "build_chunks", "simt_prep", "simt_state_fwd", "simt_out", "simt_duloc", "simt_state_bwd",
     "simt_grads", "tc_prep", "tc_state_fwd", "tc_out", "tc_chains", "tc_grads", "tc_prep_local", "decode", "tc_piece_a", "tc_piece_scan", "tc_piece_c", "l2norm", "l2norm_back",
     "linrec_fwd", "linrec_bwd", "linrec_decode", "qk_norm_rope",
-    "qk_norm_rope_bwd", "qk_norm_rope_dw"};
+    "qk_norm_rope_bwd", "qk_norm_rope_dw", "qk_norm_rope_group", "qk_norm_rope_bwd_group"};
 }  // namespace
 
 void trace_before(int32_t id, cudaStream_t stream) {

@@ -342,3 +342,23 @@ def test_rows_whose_sum_of_squares_passes_fp32(norm, dtype):
         assert (a[row] == 0).all()
         a[row] = b[row]
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("B,T", [(3, 3200), (1, 9601)])
+@pytest.mark.parametrize("Hq,Hk,d,rot,dtype,interleaved,grouped", [
+    (4, 4, 64, 64, "bf16", False, "both"), (2, 1, 128, 128, "bf16", False, "both"),
+    (1, 1, 64, 64, "bf16", True, "both"), (3, 2, 32, 32, "bf16", False, "both"),
+    (2, 2, 64, 64, "fp32", False, "both"), (1, 2, 64, 64, "fp32", True, "both"),
+    (4, 2, 64, 32, "bf16", False, "both"), (2, 1, 64, 24, "fp32", True, "both"),
+    (1, 1, 24, 24, "bf16", False, "both"), (8, 2, 64, 64, "bf16", False, "bwd"),
+    (8, 1, 64, 32, "fp32", True, "bwd"), (16, 16, 128, 128, "bf16", False, "none")])
+def test_several_tokens_per_warp_are_taken_and_right(Hq, Hk, d, rot, dtype, interleaved, grouped, B, T):
+    """The kernels that take several tokens of few heads per warp: with tokens for every warp's lanes (9600, by
+    which rows need no mask where heads and tokens fill the lanes) and with fewer in the last warp (9601)."""
+    v = draw(B, T, Hq, Hk, d, rot, dtype, seed=d + rot + Hq)
+    with gdn.LaunchTrace(16) as trace:
+        run_and_check(v, interleaved=interleaved)
+    torch.cuda.synchronize()
+    names = {"qk_norm_rope" + ("_group" if grouped == "both" else ""),
+             "qk_norm_rope_bwd" + ("" if grouped == "none" else "_group"), "qk_norm_rope_dw"}
+    assert set(trace.per_kernel()) == names
