@@ -5,6 +5,8 @@ Bounds, in units of U = 2^-24.  The norm: squares and sums of at most 8 values i
 6 joins (14, halved by the square root), root, quotient and two products (6): 16 with the weight.
 cos and sin: the angle is reduced in 64 bits, its fraction of a turn rounded to 32 bits (2 pi 2^-26)
 and the functions are good to 2 ulp: 4 U each.  A turned value: two products and a sum (2).
+The weights' gradients: as if all rows were added one after another, which holds for any order and is far
+above the sums that are made; the tests of many rows count those.
 """
 import numpy as np
 

@@ -362,3 +362,55 @@ def test_several_tokens_per_warp_are_taken_and_right(Hq, Hk, d, rot, dtype, inte
     names = {"qk_norm_rope" + ("_group" if grouped == "both" else ""),
              "qk_norm_rope_bwd" + ("" if grouped == "none" else "_group"), "qk_norm_rope_dw"}
     assert set(trace.per_kernel()) == names
+
+
+WEIGHTS = [(4, 4, 64, 64, "bf16", 9600), (4, 4, 64, 64, "bf16", 9601), (2, 1, 128, 128, "bf16", 9600),
+           (8, 2, 64, 64, "bf16", 9603), (8, 1, 64, 32, "fp32", 9601), (1, 1, 64, 64, "bf16", 9599),
+           (16, 16, 128, 128, "bf16", 3001), (3, 5, 256, 256, "fp32", 1200), (3, 3, 66, 34, "bf16", 2001),
+           (2, 2, 250, 250, "fp32", 700), (40, 3, 80, 0, "bf16", 5)]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d,rot,dtype,T", WEIGHTS)
+def test_weight_gradients_have_every_row_once(Hq, Hk, d, rot, dtype, T, interleaved):
+    """Without a norm and turned by no angle dw = sum of dy x: with whole numbers from 1 to 3 of either sign it is
+    exact in fp32 (below 9 x 9603 x 16 < 2^24 in any order), and every row left out or taken twice shows."""
+    gen = torch.Generator().manual_seed(T + d)
+
+    def whole(H):
+        n = torch.randint(1, 4, (1, T, H, d), generator=gen)
+        return torch.where(torch.rand(n.shape, generator=gen) < 0.5, n, -n)
+
+    q, k, dq, dk = whole(Hq), whole(Hk), whole(Hq), whole(Hk)
+    on = lambda t: t.to(DT[dtype]).cuda()
+    w = torch.ones(d, device="cuda")
+    f = torch.zeros(rot // 2, device="cuda") if rot else None
+    got = gdn.gdn_qk_norm_rope_bwd(on(q), on(k), on(dq), on(dk), f, norm=None, q_weight=w, k_weight=w,
+                                   interleaved=interleaved)
+    assert torch.equal(got[0], on(dq)) and torch.equal(got[1], on(dk))
+    for dw, x, dy in ((got[2], q, dq), (got[3], k, dk)):
+        assert torch.equal(dw.cpu().long(), (x * dy).sum((0, 1, 2)))
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("H,d,rot,dtype,side,T", [(4, 64, 64, "bf16", 8, 9600), (4, 64, 64, "fp32", 4, 9601),
+                                                  (16, 128, 128, "bf16", 4, 3001), (2, 250, 100, "fp32", 1, 700)])
+def test_weight_gradients_of_normalised_rows(H, d, rot, dtype, side, T, norm):
+    """dw = sum of u x r within the rounding of the sums that are made: a lane adds its rows (the 148 blocks of
+    each tensor have 8 warps, each of which takes the H heads of ceil(T / 1184) tokens at most, `side` of them in
+    lanes beside each other), then come 5 joins of lanes, 8 of warps, 5 of blocks and 32 of their sums."""
+    v = draw(1, T, H, H, d, rot, dtype, seed=T)
+    dev = {n: None if t is None else t.cuda() for n, t in v.items()}
+    kw = dict(norm=norm, **{n: dev[n] for n in ("inv_freq", "q_weight", "k_weight")})
+    got = gdn.gdn_qk_norm_rope_bwd(dev["q"], dev["k"], dev["dqo"], dev["dko"], **kw)
+    depth = -(-T // 1184) * -(-H // side) + 5 + 8 + 5 + 32
+    angle = np.arange(T, dtype=np.float64)[None, :, None, None] * np64(v["inv_freq"])
+    eps = float(np.float32(1e-6)) if norm == "rms" else 0.0
+    for x, dy, dw in ((v["q"], v["dqo"], got[2]), (v["k"], v["dko"], got[3])):
+        x, c = np64(x), 1 / d if norm == "rms" else 1.0
+        xn = x / np.sqrt(c * (x * x).sum(-1, keepdims=True) + eps)
+        u, m = ref.turn(np64(dy), angle, False, back=True)
+        err = (np.abs(xn) * ref.U * (ref.TRIG + 2) * m + ref.U * (ref.NORM + 2 + depth) * np.abs(u * xn)).sum((0, 1, 2))
+        want = (u * xn).sum((0, 1, 2))
+        assert err.max() < np.abs(u * xn).mean()  # one row of all that is left out or taken twice shows
+        close(dw, want, err, "dw")
