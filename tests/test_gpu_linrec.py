@@ -554,3 +554,11 @@ def test_gates_that_are_nan_stay_in_their_channel(types, complement, lengths):
         for got, ref_ in ((hT, want[1]), (dh0, want[4])):
             for m in range(N):
                 assert got[m, c].isnan() if m == n else got[m, c] == ref_[m, c]
+
+
+@pytest.mark.parametrize("types,complement", [(TYPES[0], True), (TYPES[1], False), (TYPES[1], True), (TYPES[2], False),
+                                              (TYPES[2], True)])
+@pytest.mark.parametrize("B,T,D", [(700, 3, 1160), (9001, 1, 260), (601, 63, 66), (1201, 16, 130)])
+def test_many_short_rows_of_every_type(B, T, D, types, complement):
+    """Streams of more rows than fill a tile, in every type and with both write strengths."""
+    run_and_check(draw(B, T, D, *types, seed=B + 1), complement=complement)
