@@ -366,8 +366,11 @@ const char *gdn_status_string(gdn_status status);
  * gdn_set_wait_limit: every bounded device-side wait (of the tensor-core kernels
  * and of gdn_linrec_*) gives up after `polls` polls of its mbarrier instead of the built-in
  * 2^23 (about a second); 0 restores the built-in limit.  A wait that gives up
- * records GDN_ERR_TIMEOUT, and the kernels of the call that start after it
- * return at once (read it with gdn_device_status).
+ * records GDN_ERR_TIMEOUT.  In gdn_fwd and gdn_bwd (read it with gdn_device_status)
+ * the kernels of the call that start after it return at once.  In gdn_linrec_*
+ * (read it with gdn_linrec_status) the CTAs of that cluster stop; the other clusters,
+ * and the backward behind a forward that recomputes the states, run on: what they
+ * write is undefined, where they write is not.
  *
  * gdn_set_test_hook: plants one failure in each later call.
  *   GDN_TEST_STALL_COPY  the first (chunk, head) CTA of the call's tensor-core

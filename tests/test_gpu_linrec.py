@@ -562,3 +562,27 @@ def test_gates_that_are_nan_stay_in_their_channel(types, complement, lengths):
 def test_many_short_rows_of_every_type(B, T, D, types, complement):
     """Streams of more rows than fill a tile, in every type and with both write strengths."""
     run_and_check(draw(B, T, D, *types, seed=B + 1), complement=complement)
+
+
+def test_a_backward_behind_a_forward_that_gave_up_runs_on_and_is_reported():
+    """Without saved states the backward recomputes them first: if that stalls, the call is undefined in its
+    values, writes nothing beside its outputs, and is reported once."""
+    v = draw(2, 3000, 72, seed=6)
+    want = run_and_check(v)[2:]
+    d = {k: t.cuda() for k, t in v.items()}
+    wide = [torch.full((2, 3000, 80), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dx, dg = (w[..., :72] for w in wide)
+    dh0 = torch.empty_like(d["h0"])
+    call = lambda: gdn.gdn_linrec_bwd(d["x"], d["g"], d["do"], h0=d["h0"], dhT=d["dhT"], grads=(dx, dg, dh0))
+    gdn.set_wait_limit(256)
+    gdn.set_test_hook(gdn.GDN_TEST_STALL_COPY)
+    try:
+        call()
+    finally:
+        gdn.set_test_hook(0)
+        gdn.set_wait_limit(0)
+    assert gdn.linrec_status() == 6 and gdn.linrec_status() == 0
+    assert all((w[..., 72:] == 7).all() for w in wide)
+    for a, b in zip(call(), want):
+        assert torch.equal(a, b)
+    assert gdn.linrec_status() == 0
