@@ -545,7 +545,7 @@ _NORMS = {None: (GDN_NORM_NONE, 0.0), "l2": (GDN_NORM_L2, 0.0), "rms": (GDN_NORM
 def _qk_plan(q, k, inv_freq, norm, eps, interleaved, index, outs, raws):
     """(descriptor, reference to it, bytes of the backward's workspace).  outs: the rotated q and
     k or their gradients, raws: the gradients of the raw q and k (None where not given)."""
-    turned = 0 if inv_freq is None else inv_freq.numel()
+    turned = None if inv_freq is None else inv_freq.shape
     key = (_rows(q, "q", index), _rows(k, "k", index), turned, norm, eps, bool(interleaved),
            _rows(outs[0], "qo", index), _rows(outs[1], "ko", index), _rows(raws[0], "dq", index),
            _rows(raws[1], "dk", index))
@@ -565,7 +565,7 @@ def _qk_plan(q, k, inv_freq, norm, eps, interleaved, index, outs, raws):
     shapes = ((B, T, Hq, d), (B, T, Hk, d))
     row = lambda t, name, i: 0 if t is None else _row_stride(t, name, q.dtype, shapes[i])
     code, default = _NORMS[norm]
-    desc = GdnQkDesc(B, T, Hq, Hk, d, 2 * turned, row(q, "q", 0), row(k, "k", 1),
+    desc = GdnQkDesc(B, T, Hq, Hk, d, 2 * turned.numel() if turned else 0, row(q, "q", 0), row(k, "k", 1),
                      row(outs[0], "qo", 0), row(outs[1], "ko", 1), row(raws[0], "dq", 0),
                      row(raws[1], "dk", 1), _DT[q.dtype], code,
                      GDN_QK_INTERLEAVED if interleaved else 0, default if eps is None else eps)

@@ -131,3 +131,15 @@ def test_head_strides():
                 torch.zeros(2, 3, 5, 8).transpose(1, 2)):
         with pytest.raises(ValueError):
             stride(bad)
+
+
+def test_refusals_do_not_depend_on_earlier_calls():
+    """Descriptors are kept by what they are made of; a call that is refused the first time is refused after
+    a like one that was not."""
+    from gated_delta_rule_99_b200._binding import _qk_plan
+    q, f = torch.zeros(1, 3, 2, 64), torch.zeros(32)
+    plan = lambda f: _qk_plan(q, q, f, "rms", None, False, -1, (None, None), (None, None))
+    for _ in range(2):
+        assert plan(f)[0].rot == 64 and plan(None)[0].rot == 0 and plan(f[:0])[0].rot == 0
+        with pytest.raises(ValueError, match="inv_freq must have one dimension"):
+            plan(f.view(2, 16))
