@@ -1048,24 +1048,28 @@ int stream_slot(cudaStream_t s) {
 }
 int slot_of(cudaStream_t s) { return capturing(s) ? 0 : stream_slot(s); }
 
-// Whether this host thread has not been told of this count yet.  It remembers the last 64 slots it asked for.
+// Whether this host thread has not been told of this count yet.  It remembers the captured calls' of every
+// device, and those of the last 64 streams it asked for.
 bool is_news(int device, int slot, uint32_t count) {
     struct Told {
-        int device, slot;
+        int device, slot;  // slot 0 where unused
         uint32_t count;
     };
     constexpr int kTold = 64;
-    thread_local Told told[kTold];  // slot 0 of device 0 with count 0 where unused
+    thread_local Told told[kTold];
+    thread_local uint32_t captured[kDevices];
     thread_local int next = 0;
-    for (Told &t : told)
-        if (t.device == device && t.slot == slot) {
-            const bool news = t.count != count;
-            t.count = count;
-            return news;
-        }
-    told[next] = {device, slot, count};
-    next = (next + 1) % kTold;
-    return count != 0;
+    uint32_t *at = slot == 0 ? &captured[device] : nullptr;
+    for (int i = 0; i < kTold && !at; ++i)
+        if (told[i].slot == slot && told[i].device == device) at = &told[i].count;
+    if (!at) {
+        told[next] = {device, slot, 0};
+        at = &told[next].count;
+        next = (next + 1) % kTold;
+    }
+    const bool news = *at != count;
+    *at = count;
+    return news;
 }
 
 // A kernel of `smem` bytes of dynamic shared memory on p's clusters.
@@ -1243,7 +1247,8 @@ gdn_status gdn_linrec_status(void *stream) {
     if (capturing(s)) return GDN_ERR_INVALID_ARG;
     int device = 0;
     void *at = nullptr;
-    if (cudaGetDevice(&device) != cudaSuccess || cudaGetSymbolAddress(&at, g_gave_up) != cudaSuccess) return GDN_ERR_CUDA;
+    if (cudaGetDevice(&device) != cudaSuccess || device >= kDevices || cudaGetSymbolAddress(&at, g_gave_up) != cudaSuccess)
+        return GDN_ERR_CUDA;
     const uint32_t *counts = static_cast<const uint32_t *>(at);
     const int slot = stream_slot(s);
     uint32_t own = 0, captured = 0;

@@ -586,3 +586,26 @@ def test_a_backward_behind_a_forward_that_gave_up_runs_on_and_is_reported():
     for a, b in zip(call(), want):
         assert torch.equal(a, b)
     assert gdn.linrec_status() == 0
+
+
+def test_a_captured_timeout_is_told_once_whatever_streams_are_asked_for():
+    v = draw(1, 2000, 64, seed=4)
+    x, g = v["x"].cuda(), v["g"].cuda()
+    gdn.set_wait_limit(256)
+    gdn.set_test_hook(gdn.GDN_TEST_STALL_COPY)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gdn.gdn_linrec_fwd(x, g)
+    finally:
+        gdn.set_test_hook(0)
+        gdn.set_wait_limit(0)
+    streams = [torch.cuda.Stream() for _ in range(24)]
+    for s in streams[:3]:
+        gdn.linrec_status(s)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert [gdn.linrec_status(s) for s in streams] == [6] + [0] * 23
+    graph.replay()
+    torch.cuda.synchronize()
+    assert [gdn.linrec_status(s) for s in streams[::-1]] == [6] + [0] * 23
