@@ -15,12 +15,16 @@
 // that runs ahead of the steps, each warp copying its own rows.
 //
 // Measured on a B200, bf16 inputs and fp32 gates (of the measured copy rate, 6.56 TB/s): 16 x 4096 x
-// 2048 forward 169 us (97%) and backward 334 us (86%); 4 x 4096 x 2048 54 us (75%) and 96 us (74%),
-// where the rows' channels alone do not fill the GPU and the exchanges show; one row of 262144 x 1024
-// 504 us (65%) and 1056 us (54%), where an exchange takes about 2600 cycles of a step of 6000.  bf16
-// gates are bound by the instructions, 22 per element forward and 47 backward: 156 us (79%) and 305 us
-// (67%) at 16 x 4096 x 2048; the write strength 1 - a costs 15 to 20% more.  Three CTAs per SM in the
-// backward, tiles twice as long or 16 warps with one CTA per SM, and one step ahead were slower.
+// 2048 forward 170 us (96%) and backward 337 us (85%); 4 x 4096 x 2048 54 us (75%) and 99 us (72%),
+// where the rows' channels alone do not fill the GPU: the first stall there is a step's two barriers, with
+// the exchange between them (a warp scheduler issues in 48 and 52% of the cycles, DRAM runs at 56 and 38% of its
+// peak); one row of 262144 x 1024 506 us (65%) and 1037 us (55%), where an exchange takes about 2600
+// cycles of a step of 6000.  bf16 gates at 16 x 4096 x 2048, with no exchange: 157 us (78%) and 307 us
+// (67%), 23 and 46 instructions per element, issued in 62 and 61% of the cycles; the rest is waits of
+// an instruction for the one before it, with the 16 warps that the registers allow.  The write
+// strength 1 - a costs 15 to 20% more.  Three CTAs per SM in the backward, tiles twice as long or
+// 16 warps with one CTA per SM, and one step ahead were slower.  The registers are at the limit of
+// two CTAs per SM: some kernels of rows off 16 bytes or in fp32 spill 4 to 28 bytes.
 //
 // A start of a sequence inside a span drops what comes before it by selection (not by a
 // factor of 0), so that no infinity or NaN crosses; padded tokens are zeros (factor

@@ -208,7 +208,7 @@ gdn_status gdn_decode(const gdn_desc *desc, const void *q, const void *k, const 
  *
  * g is the log-decay, one value per token and channel (g <= 0 in use; -inf is
  * a reset to w_t x_t; a positive g grows the state, and the products of the
- * factors over up to 128 tokens then have to stay below the fp32 maximum).
+ * factors over up to 128 tokens then have to stay within the fp32 range).
  * A NaN or infinity stays in its channel and its sequence.
  *
  * Layouts: x, o, do_, dx [B][T][D] in dtype; g, dg [B][T][D] in g_dtype
@@ -275,7 +275,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void
  * on that stream, or in a replay of captured ones on any stream of the current
  * device, that the calling host thread has not been told of (the outputs of such
  * a call are undefined); else GDN_OK.  Reading takes nothing from other threads or
- * streams.  The stream belongs to the current device and is not being captured
+ * streams.  (A thread that asks for more than 64 streams may be told again.)  The stream belongs to the current device and is not being captured
  * (GDN_ERR_INVALID_ARG).  GDN_ERR_CUDA if the stream failed. */
 gdn_status gdn_linrec_status(void *stream);
 
@@ -298,8 +298,9 @@ gdn_status gdn_linrec_decode(const gdn_linrec_desc *desc, const void *x, const v
  * i < rot / 2: (a, b) -> (a cos - b sin, a sin + b cos).  Pair i is the values i
  * and i + rot / 2, or 2 i and 2 i + 1 with GDN_QK_INTERLEAVED; values from rot on
  * are not turned.  p is the token's position (int32, any sign), or its index in
- * its row with positions NULL; the angle is formed and reduced in 64 bits, so
- * far positions are exact.  Norms and rotations are in fp32, rounded once to dtype.
+ * its row with positions NULL; the angle is formed and reduced in 64 bits (off by
+ * 3e-16 of it) and its fraction of a turn then rounded to fp32.  Norms, rotations and
+ * the sums of the weights' gradients are in fp32, rounded once to dtype.
  * |x|^2 is an fp32 sum, as GDN_FLAG_QK_L2NORM's.  A row whose sum underflows to 0
  * counts as a zero row, and below about 2^-100 the sum loses bits (where eps does
  * not cover it).  A row whose sum passes the fp32 maximum (with a value above
