@@ -1044,7 +1044,10 @@ cudaError_t fit_of(Kernel kernel, Fit *fits, const Fit **out) {
 
 bool capturing(cudaStream_t s) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) cudaGetLastError();  // the launch will say
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {  // cap says nothing; what comes next on the stream fails
+        cudaGetLastError();
+        return false;
+    }
     return cap != cudaStreamCaptureStatusNone;
 }
 int stream_slot(cudaStream_t s) {

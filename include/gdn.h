@@ -275,7 +275,9 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc *desc, const void *x, const void
  * on that stream, or in a replay of captured ones on any stream of the current
  * device, that the calling host thread has not been told of (the outputs of such
  * a call are undefined); else GDN_OK.  Reading takes nothing from other threads or
- * streams.  (A thread that asks for more than 64 streams may be told again.)  The stream belongs to the current device and is not being captured
+ * streams.  (Counted in 4095 places by the stream's handle, which two streams may
+ * share; a thread that asks for more than 64 streams may be told again.)  The
+ * stream belongs to the current device and is not being captured
  * (GDN_ERR_INVALID_ARG).  GDN_ERR_CUDA if the stream failed. */
 gdn_status gdn_linrec_status(void *stream);
 
